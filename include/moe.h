@@ -430,6 +430,106 @@ MOE_API int moe_ep_combine(moe_handle h, int T, const float *y_back, void *out, 
 MOE_API int moe_route_noalloc(int T, int d, const void *x, const float *router_w, const float *bias,
                               int32_t *idx, float *gate, int32_t *offsets, int32_t *perm, void *stream);
 
+/*
+ * ---- Stand-alone operators: the residual MoE block taken apart -----------------------
+ *
+ * The steps around and inside the experts as operators of their own, without a handle, for any
+ * number of experts and picks and with gradients: rows normalised (moe_norm_*), sorted by
+ * expert and back (moe_sort_rows, moe_unsort_rows), and few rows times 4-bit expert weights
+ * (moe_w4_matvec).  A program that trains its own experts, or serves them in 4 bits, puts its layer
+ * together from them; the sorted rows and offsets are what moe_w4_matvec reads.
+ *
+ * Conventions as at the top of this file, and:
+ *   - an element type is one of MOE_BF16, MOE_F16, MOE_F32; sums, statistics and gates are fp32, and
+ *     a result is rounded once, to its own type;
+ *   - they allocate nothing, keep nothing between calls and never block the host (moe_w4_pack does),
+ *     so they can be captured into a CUDA graph; a workspace is the caller's, holds nothing between
+ *     calls, and must not be shared by calls that may run at the same time;
+ *   - the device that holds the tensors must be the current one, and the stream one of its streams;
+ *   - results do not depend on scheduling: the same inputs give the same bits;
+ *   - an output must not overlap an input or another output (MOE_EINVAL).
+ * Common errors: MOE_EINVAL for a bad size or type, a missing or misaligned (16 bytes) pointer;
+ * MOE_ENODEV without an sm_100 device; MOE_ECUDA if a launch failed.
+ */
+#define MOE_BF16 0
+#define MOE_F16  1
+#define MOE_F32  2
+
+/*
+ * Sort the T * k routes of T tokens by expert, stably, and copy the tokens' rows into that order
+ * ("Mixture of Experts (MoELayer + Router)", the dispatch between steps 2 and 3, for any router).
+ *   x        dtype [T, d]     tokens
+ *   idx      int32 [T, k]     expert of each pick; a value outside [0, E) is a dropped route
+ *                             (a padding token, a full expert).  A token may name an expert twice.
+ *   offsets  int32 [E+1]      out: expert e has the rows offsets[e] .. offsets[e+1] - 1
+ *   perm     int32 [T*k]      out: route t * k + j of each row, -1 behind the last row
+ *   slot     int32 [T, k]     out: row of each route, -1 for a dropped one
+ *   rows     dtype [T*k, d]   out: rows[slot[t,j]] = x[t]; rows behind the last one are left as
+ *                             they were
+ * x and rows may both be NULL: the order alone.  T == 0 sets the offsets to 0.  One launch up to
+ * 1024 routes, two above.  1 <= k <= 16, 1 <= d <= 65536, T <= MOE_MAX_TOKENS; MOE_EUNSUPPORTED
+ * for E > 256.  The gradient of x is moe_unsort_rows of the rows' gradient with gate = NULL.
+ */
+MOE_API int moe_sort_rows(int dtype, int T, int k, int E, int d, const void *x, const int32_t *idx,
+                          int32_t *offsets, int32_t *perm, int32_t *slot, void *rows, void *stream);
+
+/*
+ * The rows back in token order, each times its gate, summed in pick order (step 4 of the MoE section):
+ *   out[t] = sum_j gate[t,j] * rows[slot[t,j]]
+ *   rows  rows_dtype [T*k, d]  rows_dtype is dtype or MOE_F32 (else MOE_EUNSUPPORTED)
+ *   slot  int32 [T, k]         as moe_sort_rows wrote it; a value outside [0, T*k) is a dropped
+ *                              route, which adds nothing whatever its gate and row hold
+ *   gate  fp32 [T, k]          or NULL: every gate 1
+ *   out   dtype [T, d]         a token without routes gets 0
+ */
+MOE_API int moe_unsort_rows(int rows_dtype, int dtype, int T, int k, int d, const void *rows, const int32_t *slot,
+                            const float *gate, void *out, void *stream);
+
+/*
+ * The gradient of moe_unsort_rows:
+ *   drows[slot[t,j]] = gate[t,j] * dout[t],   dgate[t,j] = sum_c dout[t,c] * rows[slot[t,j],c]
+ *   dout   dtype [T, d]
+ *   rows   rows_dtype [T*k, d]  the forward call's rows; may be NULL when dgate is
+ *   drows  rows_dtype [T*k, d]  out; rows that no route points to are left as they were
+ *   dgate  fp32 [T, k]          out, 0 for a dropped route; NULL: not wanted
+ * No two routes may have the same slot.
+ */
+MOE_API int moe_unsort_rows_backward(int rows_dtype, int dtype, int T, int k, int d, const void *dout,
+                                     const void *rows, const int32_t *slot, const float *gate, void *drows,
+                                     float *dgate, void *stream);
+
+#define MOE_NORM_RMS   0   /* y = x / sqrt(mean(x^2) + eps) * gain, as around the MoE in the residual block */
+#define MOE_NORM_LAYER 1   /* y = (x - mean(x)) / sqrt(mean((x - mean)^2) + eps) * gain + bias             */
+
+/*
+ * Normalise T rows of width d ("Transformer stack and language model head": the norms around the MoE).
+ *   x      dtype [T, d]
+ *   gain   dtype [d]     or NULL: 1
+ *   bias   dtype [d]     or NULL: 0; MOE_NORM_LAYER only (else MOE_EINVAL)
+ *   y      dtype [T, d]  out
+ *   stats  fp32  [T, 2]  out: the row's mean (0 for MOE_NORM_RMS) and 1 / sqrt(... + eps), which the
+ *                        backward pass takes; or NULL
+ * 1 <= d <= 65536, T <= MOE_MAX_TOKENS, eps >= 0.  Statistics are taken in fp32, the variance around
+ * the mean.  T == 0 is a no-op.
+ */
+MOE_API int moe_norm_forward(int kind, int dtype, int T, int d, const void *x, const void *gain, const void *bias,
+                             float eps, void *y, float *stats, void *stream);
+
+/*
+ * The gradient of moe_norm_forward at the same x, gain and stats.
+ *   dy         dtype [T, d]
+ *   dx         dtype [T, d]  out
+ *   dgain      fp32 [d]      out: sum over rows of dy * (x - mean) * rstd; NULL: not wanted
+ *   dbias      fp32 [d]      out: sum over rows of dy; NULL: not wanted; MOE_NORM_LAYER only
+ *   workspace  device buffer of moe_norm_workspace(T, d) bytes
+ * T == 0 sets dgain and dbias to 0 (the other pointers may then be NULL).
+ */
+MOE_API int moe_norm_backward(int kind, int dtype, int T, int d, const void *x, const void *gain, const float *stats,
+                              const void *dy, void *dx, float *dgain, float *dbias, void *workspace, void *stream);
+
+/* Bytes of the workspace of moe_norm_backward, or MOE_EINVAL for a bad size.  Needs no device. */
+MOE_API long long moe_norm_workspace(int T, int d);
+
 #ifdef __cplusplus
 }
 #endif

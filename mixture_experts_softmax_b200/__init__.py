@@ -31,6 +31,11 @@ MOE_MAX_TOKENS = 262144
 MOE_LAYOUT_IN_OUT = 0
 MOE_LAYOUT_PACKED = 1
 MOE_NOALLOC_MAX_TOKENS = 65536
+MOE_BF16 = 0
+MOE_F16 = 1
+MOE_F32 = 2
+MOE_NORM_RMS = 0
+MOE_NORM_LAYER = 1
 
 KERNEL_NAMES = ("router", "dispatch", "gather", "up_proj", "down_proj", "combine", "prenorm", "route_small")
 
@@ -43,6 +48,8 @@ EXPORTS = (
     "moe_set_weight_layout", "moe_pack_weight", "moe_route_noalloc",
     "moe_ep_dispatch", "moe_ep_experts", "moe_ep_combine", "moe_set_cta_pairs", "moe_pack_weight_n",
     "moe_set_host_overlap", "moe_host_wait",
+    "moe_sort_rows", "moe_unsort_rows", "moe_unsort_rows_backward",
+    "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace",
 )
 
 
@@ -87,6 +94,12 @@ def _load() -> ctypes.CDLL:
         "moe_set_cta_pairs": (I, [P, I]),
         "moe_set_host_overlap": (I, [P, I]),
         "moe_host_wait": (I, [P, P]),
+        "moe_sort_rows": (I, [I, I, I, I, I, P, P, P, P, P, P, P]),
+        "moe_unsort_rows": (I, [I, I, I, I, I, P, P, P, P, P]),
+        "moe_unsort_rows_backward": (I, [I, I, I, I, I, P, P, P, P, P, P, P]),
+        "moe_norm_forward": (I, [I, I, I, I, P, P, P, F, P, P, P]),
+        "moe_norm_backward": (I, [I, I, I, I, P, P, P, P, P, P, P, P, P]),
+        "moe_norm_workspace": (ctypes.c_longlong, [I, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -276,6 +289,84 @@ def moe_ep_experts(h, n_src, E_local, recv_counts, recv_rows, w_lin, s_lin, w_v,
 
 def moe_ep_combine(h, T, y_back, out, stream=None) -> int:
     return _lib.moe_ep_combine(h, int(T), _ptr(y_back), _ptr(out), _stream(stream))
+
+
+# ---- stand-alone operators ---------------------------------------------------------------------
+# They take the same arguments as their C entry points.  A torch tensor passed to one of them has to
+# be what the C side reads: dense, on the current CUDA device, of the named element type and at
+# least as long as the call's sizes say; anything else raises ValueError.  Integers are raw addresses.
+
+_DTYPES = None
+
+
+def _dtype_of(code):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {MOE_BF16: torch.bfloat16, MOE_F16: torch.float16, MOE_F32: torch.float32,
+                   "i32": torch.int32, "i8": torch.int8, "u8": torch.uint8}
+    return _DTYPES.get(code)
+
+
+def _arg(t, name, code, numel):
+    """Address of one operand.  code: its element type; numel: the elements that the call may touch."""
+    if t is None or isinstance(t, int):
+        return t
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name}: cannot pass {type(t).__name__} as a pointer")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a dense CUDA tensor")
+    want = _dtype_of(code)
+    if want is not None and t.dtype is not want:
+        raise ValueError(f"{name}: {t.dtype}, needs {want}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, needs {numel}")
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, which is not the current device")
+    return t.data_ptr()
+
+
+def moe_sort_rows(dtype, T, k, E, d, x, idx, offsets, perm, slot, rows, stream=None) -> int:
+    n = T * k
+    return _lib.moe_sort_rows(dtype, T, k, E, d, _arg(x, "x", dtype, T * d), _arg(idx, "idx", "i32", n),
+                              _arg(offsets, "offsets", "i32", E + 1), _arg(perm, "perm", "i32", n),
+                              _arg(slot, "slot", "i32", n), _arg(rows, "rows", dtype, n * d), _stream(stream))
+
+
+def moe_unsort_rows(rows_dtype, dtype, T, k, d, rows, slot, gate, out, stream=None) -> int:
+    """Also the gradient of moe_sort_rows' x: rows = the rows' gradient, gate = None."""
+    n = T * k
+    return _lib.moe_unsort_rows(rows_dtype, dtype, T, k, d, _arg(rows, "rows", rows_dtype, n * d),
+                                _arg(slot, "slot", "i32", n), _arg(gate, "gate", MOE_F32, n),
+                                _arg(out, "out", dtype, T * d), _stream(stream))
+
+
+def moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, dout, rows, slot, gate, drows, dgate, stream=None) -> int:
+    n = T * k
+    return _lib.moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, _arg(dout, "dout", dtype, T * d),
+                                         _arg(rows, "rows", rows_dtype, n * d), _arg(slot, "slot", "i32", n),
+                                         _arg(gate, "gate", MOE_F32, n), _arg(drows, "drows", rows_dtype, n * d),
+                                         _arg(dgate, "dgate", MOE_F32, n), _stream(stream))
+
+
+def moe_norm_forward(kind, dtype, T, d, x, gain, bias, eps, y, stats=None, stream=None) -> int:
+    return _lib.moe_norm_forward(kind, dtype, T, d, _arg(x, "x", dtype, T * d), _arg(gain, "gain", dtype, d),
+                                 _arg(bias, "bias", dtype, d), eps, _arg(y, "y", dtype, T * d),
+                                 _arg(stats, "stats", MOE_F32, 2 * T), _stream(stream))
+
+
+def moe_norm_backward(kind, dtype, T, d, x, gain, stats, dy, dx, dgain, dbias, workspace, stream=None) -> int:
+    return _lib.moe_norm_backward(kind, dtype, T, d, _arg(x, "x", dtype, T * d), _arg(gain, "gain", dtype, d),
+                                  _arg(stats, "stats", MOE_F32, 2 * T), _arg(dy, "dy", dtype, T * d),
+                                  _arg(dx, "dx", dtype, T * d), _arg(dgain, "dgain", MOE_F32, d),
+                                  _arg(dbias, "dbias", MOE_F32, d),
+                                  _arg(workspace, "workspace", "u8", moe_norm_workspace(T, d)), _stream(stream))
+
+
+def moe_norm_workspace(T, d) -> int:
+    """Bytes (a uint8 tensor's length) of moe_norm_backward's workspace, or a negative status."""
+    return _lib.moe_norm_workspace(T, d)
 
 
 def moe_plan(h, T: int):

@@ -1,0 +1,195 @@
+"""RMSNorm and LayerNorm rows and their gradients (moe_norm_forward, moe_norm_backward) against plain
+64-bit forms: rows held by a warp, by a block and read again, every vector width and type."""
+import pytest
+import torch
+
+from tests import ops64
+from tests.test_gpu_rows import DT, guarded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_softmax_b200 as m
+    return m
+
+
+def inputs(T, d, dt, layer, seed=0):
+    g = torch.Generator().manual_seed(seed + T * 7 + d)
+    x = (torch.randn((T, d), generator=g) * (0.2 + 3 * torch.rand((T, 1), generator=g))
+         + torch.randn((1, d), generator=g)).to(DT[dt])
+    gain = (1 + 0.3 * torch.randn(d, generator=g)).to(DT[dt])
+    bias = (0.3 * torch.randn(d, generator=g)).to(DT[dt]) if layer else None
+    return x, gain, bias, torch.randn((T, d), generator=g).to(DT[dt])
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+def run_forward(m, kind, dt, x, gain, bias, eps=1e-5):
+    T, d = x.shape
+    y, c0 = guarded((T, d), DT[dt], 99.0)
+    stats, c1 = guarded((T, 2), torch.float32, 99.0)
+    m.check(m.moe_norm_forward(kind, dt, T, d, x.cuda(), cuda(gain), cuda(bias), eps, y, stats), "moe_norm_forward")
+    torch.cuda.synchronize()
+    c0()
+    c1()
+    return y.cpu(), stats.cpu()
+
+
+def run_backward(m, kind, dt, x, gain, stats, dy, want_bias):
+    T, d = x.shape
+    dx, c0 = guarded((T, d), DT[dt], 99.0)
+    dgain, c1 = guarded((d,), torch.float32, 99.0)
+    dbias, c2 = guarded((d,), torch.float32, 99.0)
+    ws, c3 = guarded((m.moe_norm_workspace(T, d),), torch.uint8, 255)   # nan, read as fp32
+    m.check(m.moe_norm_backward(kind, dt, T, d, x.cuda(), cuda(gain), stats.cuda(), dy.cuda(), dx, dgain,
+                                dbias if want_bias else None, ws), "moe_norm_backward")
+    torch.cuda.synchronize()
+    for c in (c0, c1, c2, c3):
+        c()
+    return dx.cpu(), dgain.cpu(), dbias.cpu()
+
+
+# a warp a row (by 16-, 4- and 2-byte vectors, and single elements), a block a row, rows read again
+SIZES = [(1, 1), (1, 6144), (3, 2), (5, 37), (9, 256), (17, 1024), (130, 1030), (33, 1537), (65, 4104), (700, 520), (700, 2560),
+         (2, 8191), (3, 16384), (5, 16392), (2, 33000), (1, 40001), (2, 65536)]
+
+
+@pytest.mark.parametrize("T,d", SIZES)
+@pytest.mark.parametrize("dt", [0, 1, 2])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_norm(m, T, d, dt, kind):
+    x, gain, bias, dy = inputs(T, d, dt, kind == 1)
+    y, stats = run_forward(m, kind, dt, x, gain, bias)
+    ref, rstats, tol, tstats = ops64.norm(x, gain, bias, float(torch.tensor(1e-5)), kind == 1, DT[dt])
+    ops64.assert_close(stats, rstats, tstats, "stats")
+    ops64.assert_close(y, ref, tol, "y")
+    got = run_backward(m, kind, dt, x, gain, stats, dy, kind == 1)
+    want, tols = ops64.norm_grad(x, gain, stats, dy, kind == 1, DT[dt])
+    ops64.assert_close(got[0], want[0], tols[0], "dx")
+    ops64.assert_close(got[1], want[1], tols[1], "dgain")
+    if kind == 1:
+        ops64.assert_close(got[2], want[2], tols[2], "dbias")
+
+
+@pytest.mark.parametrize("T,d", [(3000, 96), (2500, 8200), (4000, 19), (1300, 6144), (1000, 16400)])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_norm_many_rows(m, T, d, kind):
+    """More rows than blocks: every block sums over several."""
+    x, gain, bias, dy = inputs(T, d, 0, kind == 1)
+    y, stats = run_forward(m, kind, 0, x, gain, bias)
+    ref, _, tol, _ = ops64.norm(x, gain, bias, float(torch.tensor(1e-5)), kind == 1, DT[0])
+    ops64.assert_close(y, ref, tol, "y")
+    got = run_backward(m, kind, 0, x, gain, stats, dy, kind == 1)
+    want, tols = ops64.norm_grad(x, gain, stats, dy, kind == 1, DT[0])
+    for a, b, t in list(zip(got, want, tols))[:2 + kind]:
+        ops64.assert_close(a, b, t)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_norm_without_gain_bias_stats(m, kind):
+    x, _, _, dy = inputs(20, 384, 0, False)
+    y = torch.empty((20, 384), dtype=torch.bfloat16, device="cuda")
+    m.check(m.moe_norm_forward(kind, 0, 20, 384, x.cuda(), None, None, 1e-6, y, None))
+    ref, rstats, tol, _ = ops64.norm(x, None, None, float(torch.tensor(1e-6)), kind == 1, DT[0])
+    ops64.assert_close(y.cpu(), ref, tol)
+    stats = rstats.float()
+    dx = torch.empty_like(y)
+    ws = torch.empty(m.moe_norm_workspace(20, 384), dtype=torch.uint8, device="cuda")
+    m.check(m.moe_norm_backward(kind, 0, 20, 384, x.cuda(), None, stats.cuda(), dy.cuda(), dx, None, None, ws))
+    want, tols = ops64.norm_grad(x, None, stats, dy, kind == 1, DT[0])
+    ops64.assert_close(dx.cpu(), want[0], tols[0])
+
+
+def test_dbias_alone_and_dgain_alone(m):
+    x, gain, bias, dy = inputs(50, 200, 2, True)
+    _, stats = run_forward(m, 1, 2, x, gain, bias)
+    full = run_backward(m, 1, 2, x, gain, stats, dy, True)
+    ws = torch.empty(m.moe_norm_workspace(50, 200), dtype=torch.uint8, device="cuda")
+    for which in (1, 2):
+        out = torch.empty(200, device="cuda")
+        dx = torch.empty((50, 200), device="cuda")
+        m.check(m.moe_norm_backward(1, 2, 50, 200, x.cuda(), gain.cuda(), stats.cuda(), dy.cuda(), dx,
+                                    out if which == 1 else None, out if which == 2 else None, ws))
+        assert torch.equal(out.cpu(), full[which]) and torch.equal(dx.cpu(), full[0])
+
+
+def test_no_rows(m):
+    g, b = torch.ones(64, device="cuda"), torch.ones(64, device="cuda")
+    m.check(m.moe_norm_forward(0, 0, 0, 64, None, None, None, 1e-5, None))
+    m.check(m.moe_norm_backward(1, 0, 0, 64, None, None, None, None, None, g, b, None))
+    assert (g == 0).all() and (b == 0).all()
+
+
+def test_constant_and_offset_rows(m):
+    """A constant row has variance 0: y = bias, whatever its size; a large mean does not cost the variance."""
+    x = torch.full((4, 512), 1000.0)
+    x[2:] = 4096.0 + torch.randn((2, 512), generator=torch.Generator().manual_seed(0)) * 2.0 ** -3
+    gain, bias = torch.full((512,), 2.0), torch.full((512,), 0.5)
+    y, stats = run_forward(m, 1, 2, x, gain, bias)
+    assert (y[:2] == 0.5).all() and (stats[:2, 0] == 1000.0).all()
+    ref, _, tol, _ = ops64.norm(x, gain, bias, float(torch.tensor(1e-5)), True, torch.float32)
+    ops64.assert_close(y, ref, tol)
+    # The bound by arithmetic: the mean may be off by 80 * 2^-24 * 4096 = 0.0195, which is 0.16 of the rows'
+    # deviation of 1/8 (times the gain of 2: 0.31), and the variance by 2 * 0.0195 * mean|c| = 0.0195 / 5 of
+    # 1/64, a quarter: an eighth of |y - bias| <= 7.5, 0.94.  A difference of squares would be off by
+    # 2^-24 * 4096^2 = 1, 64 times the variance.
+    assert tol[2:].max() < 0.31 + 0.94 + 0.25
+
+
+def test_nonfinite_rows_stay_in_their_row(m):
+    x, gain, bias, dy = inputs(12, 300, 0, True)
+    x[3, 7] = float("nan")
+    x[8, 100] = float("inf")
+    y, stats = run_forward(m, 1, 0, x, gain, bias)
+    ok = [t for t in range(12) if t not in (3, 8)]
+    assert y[3].isnan().all() and y[8].isnan().any()
+    assert y[ok].isfinite().all() and stats[ok].isfinite().all()
+
+
+@pytest.mark.parametrize("layer", [False, True])
+def test_gradient_against_differences(m, layer):
+    """The products of the gradients with random directions against central differences of the 64-bit form."""
+    T, d, eps = 6, 40, float(torch.tensor(1e-5))
+    x, gain, bias, dy = inputs(T, d, 2, layer)
+    _, stats = run_forward(m, int(layer), 2, x, gain, bias)
+    dx, dgain, dbias = (t.double() for t in run_backward(m, int(layer), 2, x, gain, stats, dy, layer))
+    g = torch.Generator().manual_seed(9)
+    u, v, w = (torch.randn(s, generator=g).double() for s in ((T, d), (d,), (d,)))
+
+    def f(h):
+        b = bias.double() + h * w if layer else None
+        return (ops64.norm(x.double() + h * u, gain.double() + h * v, b, eps, layer, torch.float32)[0] * dy.double()).sum()
+    h = 2.0 ** -12
+    diff = (8 * (f(h) - f(-h)) - (f(2 * h) - f(-2 * h))) / (12 * h)
+    terms = torch.cat([(dx * u).flatten(), dgain * v, (dbias * w) if layer else torch.zeros(1).double()])
+    # fp32 gradients and statistics: 200 roundings on each term's size; the differences leave h^4 of the
+    # fifth derivative, whose scale is (1 / sd)^5 < 2^12 here: 2^-36 of the terms
+    sizes = (dy.double().abs() * stats[:, 1:].double() * u.abs()).sum() * 4 * gain.abs().max() + terms.abs().sum() \
+        + (dy.double().abs() * 4).sum() * v.abs().max()
+    assert abs(terms.sum() - diff) <= 200 * ops64.U * sizes
+
+
+def test_offsets_pass_32_bits(m):
+    """Rows beyond 2^31 elements: the last rows of 262,144 x 8,704 against the same rows alone."""
+    T, d = 262144, 8704
+    x = torch.ones((T, d), dtype=torch.bfloat16, device="cuda")
+    tail, gain, _, dy = inputs(16, d, 0, False)
+    x[-16:] = tail.cuda()
+    y = torch.empty_like(x)
+    stats = torch.empty((T, 2), device="cuda")
+    m.check(m.moe_norm_forward(0, 0, T, d, x, gain.cuda(), None, 1e-5, y, stats))
+    want, wstats = run_forward(m, 0, 0, tail, gain, None)
+    assert torch.equal(y[-16:].cpu(), want) and torch.equal(stats[-16:].cpu(), wstats)
+    g = torch.zeros_like(x)
+    g[-16:] = dy.cuda()
+    dgain = torch.empty(d, device="cuda")
+    ws = torch.empty(m.moe_norm_workspace(T, d), dtype=torch.uint8, device="cuda")
+    m.check(m.moe_norm_backward(0, 0, T, d, x, gain.cuda(), stats, g, y, dgain, None, ws))
+    dx, dg, _ = run_backward(m, 0, 0, tail, gain, wstats, dy, False)
+    assert torch.equal(y[-16:].cpu(), dx) and (y[:-16] == 0).all()
+    _, tols = ops64.norm_grad(tail, gain, wstats, dy, False, DT[0])
+    ops64.assert_close(dgain.cpu(), dg.double(), 2 * tols[1])
