@@ -530,6 +530,37 @@ MOE_API int moe_norm_backward(int kind, int dtype, int T, int d, const void *x, 
 /* Bytes of the workspace of moe_norm_backward, or MOE_EINVAL for a bad size.  Needs no device. */
 MOE_API long long moe_norm_workspace(int T, int d);
 
+/*
+ * Products of few rows with 4-bit weights ("Quantized weights", w.weight * w.scales, in half the bytes): a
+ * weight is a value q in [-8, 7] times a bf16 scale shared by `group` consecutive inputs of an output
+ * feature, group = 32, 64 or 128 (else MOE_EUNSUPPORTED); the last group may be shorter.
+ *
+ * moe_w4_pack lays the weights of E experts out for moe_w4_matvec, once, when they are loaded:
+ *   q       int8 [E, K, N]                 (x @ W orientation)
+ *   scales  bf16 [E, ceil(K / group), N]
+ *   packed  buffer of moe_w4_packed_bytes(E, K, N, group) bytes (negative: that status)
+ * It synchronises `stream` and returns MOE_ERANGE if a value lies outside [-8, 7] (packed is then not
+ * usable).  1 <= K, N <= 131072; MOE_EUNSUPPORTED for E > 1024.
+ */
+MOE_API long long moe_w4_packed_bytes(int E, int K, int N, int group);
+MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t *q, const void *scales, void *packed, void *stream);
+
+/*
+ * Each expert's rows times its 4-bit weights ("Mixture of Experts (MoELayer + Router)", step 3):
+ *   y[r, n] = sum_k x[r, k] * q[e, k, n] * s[e, k / group, n]     offsets[e] <= r < offsets[e+1]
+ * and with packed_v the gated up-projection, gelu(x W) * (x Wv) with the tanh form of gelu.
+ *   x         dtype [R, K]      MOE_BF16 or MOE_F16
+ *   offsets   int32 [E+1]       the experts' row ranges, on the device (moe_sort_rows writes them); values
+ *                               outside [0, R] are clamped, a row in two ranges gets either product;
+ *                               NULL with E == 1: all rows
+ *   packed, packed_v            from moe_w4_pack with the same E, K, N, group; packed_v may be NULL
+ *   y         out_dtype [R, N]  out: dtype or MOE_F32; rows of no expert are left as they were
+ * Made for a few rows an expert: 32 rows share one pass over the weights.  R <= 1024 (else
+ * MOE_EUNSUPPORTED).  R == 0 is a no-op.  Sums are fp32.
+ */
+MOE_API int moe_w4_matvec(int dtype, int out_dtype, int E, int K, int N, int group, int R, const void *x,
+                          const int32_t *offsets, const void *packed, const void *packed_v, void *y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,6 +50,7 @@ EXPORTS = (
     "moe_set_host_overlap", "moe_host_wait",
     "moe_sort_rows", "moe_unsort_rows", "moe_unsort_rows_backward",
     "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace",
+    "moe_w4_packed_bytes", "moe_w4_pack", "moe_w4_matvec",
 )
 
 
@@ -100,6 +101,9 @@ def _load() -> ctypes.CDLL:
         "moe_norm_forward": (I, [I, I, I, I, P, P, P, F, P, P, P]),
         "moe_norm_backward": (I, [I, I, I, I, P, P, P, P, P, P, P, P, P]),
         "moe_norm_workspace": (ctypes.c_longlong, [I, I]),
+        "moe_w4_packed_bytes": (ctypes.c_longlong, [I, I, I, I]),
+        "moe_w4_pack": (I, [I, I, I, I, P, P, P, P]),
+        "moe_w4_matvec": (I, [I, I, I, I, I, I, I, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -367,6 +371,25 @@ def moe_norm_backward(kind, dtype, T, d, x, gain, stats, dy, dx, dgain, dbias, w
 def moe_norm_workspace(T, d) -> int:
     """Bytes (a uint8 tensor's length) of moe_norm_backward's workspace, or a negative status."""
     return _lib.moe_norm_workspace(T, d)
+
+
+def moe_w4_packed_bytes(E, K, N, group) -> int:
+    """Bytes (a uint8 tensor's length) of packed 4-bit weights, or a negative status."""
+    return _lib.moe_w4_packed_bytes(E, K, N, group)
+
+
+def moe_w4_pack(E, K, N, group, q, scales, packed, stream=None) -> int:
+    """q int8 [E, K, N] in [-8, 7], scales bf16 [E, ceil(K / group), N] -> packed uint8."""
+    return _lib.moe_w4_pack(E, K, N, group, _arg(q, "q", "i8", E * K * N),
+                            _arg(scales, "scales", MOE_BF16, E * -(-K // max(group, 1)) * N),
+                            _arg(packed, "packed", "u8", moe_w4_packed_bytes(E, K, N, group)), _stream(stream))
+
+
+def moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, x, offsets, packed, packed_v, y, stream=None) -> int:
+    nbytes = moe_w4_packed_bytes(E, K, N, group)
+    return _lib.moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, _arg(x, "x", dtype, R * K),
+                              _arg(offsets, "offsets", "i32", E + 1), _arg(packed, "packed", "u8", nbytes),
+                              _arg(packed_v, "packed_v", "u8", nbytes), _arg(y, "y", out_dtype, R * N), _stream(stream))
 
 
 def moe_plan(h, T: int):

@@ -1,0 +1,507 @@
+// w4.cu -- few rows times 4-bit expert weights with group scales:
+//
+//   y[r, n] = sum_k x[r, k] * q[e, k, n] * s[e, k / G, n]      for the rows r of expert e
+//   gated:    gelu(x W) * (x Wv), the up-projection of the MoE section's step 3
+//
+// With few rows the weights' bytes bound it: each is read once, by asynchronous 16-byte copies into
+// a ring of stages that every lane keeps for itself, so that the copies of the next stages run while one is
+// multiplied.  The products run on mma.sync m16n8k16 with 16 features as rows and 8 token rows as
+// columns: a weight enters as the exact 16-bit float of its value, the fp32 sum over one group is
+// multiplied by the group's scale and added up in fp32.  (The tcgen05 path wants both operands
+// staged as 16-bit tiles; for 8 columns that staging alone moves four times the weights' bytes through shared memory.)
+//
+// Packed layout (moe_w4_pack).  Features in blocks of 32, inputs in units of 128 (padded: value 0,
+// scale 0).  A unit of a block is 2 KB, in the order of the lanes' multiply operands: input chunk of
+// 64 (2) x feature tile of 16 (2) x lane (32) x step of 16 inputs (4 words).  Lane 4 g + c of the step
+// holds the inputs 4 c .. 4 c + 3 of features g and g + 8: nibble i and i + 4 of its word are operand
+// register i's first and second element, stored as value + 8.  The scales follow all weights:
+// per block and group 32 bf16, in the order 4 g + i for feature g + 8 i.
+#include <cooperative_groups.h>
+
+#include "ops_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+
+namespace {
+
+constexpr int kBlockF = 32;            // features of a block: one warp's
+constexpr int kUnitK = 128;            // inputs of a unit: one stage
+constexpr int kUnitBytes = kBlockF * kUnitK / 2;
+constexpr int kStages = 4;
+constexpr int kWarps = 8;
+constexpr int kMaxRows = 1024;
+constexpr int kMaxWExperts = 1024;
+constexpr int kXUnits = 16;            // units of one 8-row slab of staged x; fewer with more slabs
+constexpr int kRedStride = 36;         // floats per row of a warp's partial sums: no bank conflicts
+constexpr int kTail = 256;             // bytes behind the scales: the packing's range flag
+
+struct W4Shape {
+    int E, K, N, G;
+    int blocks, units, per_unit;       // feature blocks, input units, groups of a unit
+    size_t scales;                     // byte offset of the scales
+    size_t bytes;
+};
+
+W4Shape shape_of(int E, int K, int N, int G)
+{
+    W4Shape s{E, K, N, G, (N + kBlockF - 1) / kBlockF, (K + kUnitK - 1) / kUnitK, kUnitK / G, 0, 0};
+    const size_t u = static_cast<size_t>(E) * s.blocks * s.units;
+    s.scales = u * kUnitBytes;
+    s.bytes = s.scales + u * s.per_unit * kBlockF * 2 + kTail;
+    return s;
+}
+
+// ---- packing -----------------------------------------------------------------------
+
+// one thread a 32-bit word: lanes of a warp cover the 32 features of 8 inputs
+__global__ void __launch_bounds__(256) w4_pack_kernel(W4Shape s, const int8_t *q, uint32_t *out, int *flag)
+{
+    const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+    const size_t total = static_cast<size_t>(s.E) * s.blocks * s.units * (kUnitBytes / 4);
+    if (i >= total) return;
+    // reading order: feature tile and row (16), then the two low bits of the input position
+    const int g = i & 7, tile = (i >> 3) & 1, c = (i >> 4) & 3, step = (i >> 6) & 3, chunk = (i >> 8) & 1;
+    const size_t unit = i >> 9;
+    const int u = static_cast<int>(unit % s.units);
+    const size_t eb = unit / s.units;
+    const int b = static_cast<int>(eb % s.blocks), e = static_cast<int>(eb / s.blocks);
+    const int k0 = u * kUnitK + chunk * 64 + step * 16 + c * 4, n0 = b * kBlockF + tile * 16 + g;
+    const int8_t *p = q + static_cast<size_t>(e) * s.K * s.N;
+    uint32_t w = 0;
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)          // operand register: feature + 8 for odd ones, inputs + 2 for the upper two
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {    // its low and high half
+            const int n = n0 + (r & 1) * 8, k = k0 + (r >> 1) * 2 + h;
+            const int v = n < s.N && k < s.K ? p[static_cast<size_t>(k) * s.N + n] : 0;
+            bad |= v < -8 || v > 7;
+            w |= static_cast<uint32_t>((v + 8) & 15) << (4 * r + 16 * h);
+        }
+    if (bad) *flag = 1;
+    out[unit * (kUnitBytes / 4) + ((chunk * 2 + tile) * 32 + g * 4 + c) * 4 + step] = w;
+}
+
+__global__ void __launch_bounds__(256) w4_pack_scales_kernel(W4Shape s, const __nv_bfloat16 *in, __nv_bfloat16 *out)
+{
+    const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+    const size_t total = static_cast<size_t>(s.E) * s.blocks * s.units * s.per_unit * kBlockF;
+    if (i >= total) return;
+    const int f = i & 31;                // feature; written to place 4 g + i of feature g + 8 i
+    const size_t group = i >> 5;
+    const int groups = (s.K + s.G - 1) / s.G, padded = s.units * s.per_unit;
+    const int gr = static_cast<int>(group % padded);
+    const size_t eb = group / padded;
+    const int n = static_cast<int>(eb % s.blocks) * kBlockF + f;
+    const int e = static_cast<int>(eb / s.blocks);
+    const bool real = n < s.N && gr < groups;
+    out[group * kBlockF + (f & 7) * 4 + (f >> 3)] =
+        real ? in[(static_cast<size_t>(e) * groups + gr) * s.N + n] : __float2bfloat16_rn(0.f);
+}
+
+// ---- the product ---------------------------------------------------------------------
+
+struct W4Args {
+    int E, K, N, R;
+    int blocks, units;
+    size_t scales;
+    const void *x;              // [R, K]
+    const int *offsets;         // [E + 1] or nullptr: one expert, all rows
+    const uint8_t *w, *wv;
+    void *y;                    // [R, N]
+    int out_f32;
+    int splits;                 // blocks of a cluster, each with its share of the units
+    int kparts;                 // warps of a block that share a feature block's units
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+
+// Two 4-bit values of w (bits 4 i .. and 16 + 4 i ..) as exact 16-bit floats: OR-ed into the mantissa of
+// 128 (bf16) or 1024 (fp16), whose last place is 1, then 128 + 8 (1024 + 8) subtracted.
+template <class T> struct Deq;
+template <> struct Deq<__nv_bfloat16> {
+    template <int I>
+    static __device__ __forceinline__ uint32_t pair(uint32_t w)
+    {
+        uint32_t v = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&v), __floats2bfloat162_rn(136.f, 136.f));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Deq<__half> {
+    template <int I>
+    static __device__ __forceinline__ uint32_t pair(uint32_t w)
+    {
+        uint32_t v = ((w >> (4 * I)) & 0x000f000fu) | 0x64006400u;
+        const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&v), __floats2half2_rn(1032.f, 1032.f));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// x rows [row0, row0 + rows) at inputs [k0, k0 + nk) into shared memory, in the order in which a lane takes its
+// operands: within 64 inputs, input 16 j + 4 c + i at place 16 c + 4 j + i.  Inputs behind K are 0 (the
+// weights there are too, but 0 times what the memory holds need not be).
+__device__ __forceinline__ void stage_x(const W4Args &a, char *xs, int stride, int row0, int rows, int k0, int nk)
+{
+    const uint16_t *x = static_cast<const uint16_t *>(a.x);
+    const int per_row = nk / 8;
+    for (int p = threadIdx.x; p < rows * per_row; p += kWarps * 32) {
+        const int r = p / per_row, kk = (p - r * per_row) * 8, k = k0 + kk;
+        const uint16_t *src = x + static_cast<size_t>(row0 + r) * a.K + k;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if ((a.K & 7) == 0) {
+            if (k < a.K) v = __ldg(reinterpret_cast<const uint4 *>(src));
+        } else {
+            uint16_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = k + i < a.K ? __ldg(src + i) : static_cast<uint16_t>(0);
+            v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+        const int j = (kk >> 4) & 3, c = (kk >> 2) & 3;   // c is 0 or 2
+        char *dst = xs + r * stride + (kk >> 6) * 128 + c * 32 + j * 8;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2 *>(dst + 32) = make_uint2(v.z, v.w);
+    }
+}
+
+__device__ __forceinline__ float gelu_of(float a)
+{
+    // 0.5 a (1 + tanh(z)) = a / (1 + exp(-2 z)),  z = sqrt(2 / pi) (a + 0.044715 a^3)
+    const float k0 = 0.7978845608028654f, k1 = 0.044715f * 0.7978845608028654f;
+    const float z = a * fmaf(k1, a * a, k0);
+    return a / (1.f + expf(-2.f * z));
+}
+
+// One pass over the block's share of the weights for up to 8 NB rows.
+template <class T, int G, bool GATED, int NB>
+__device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int row0, int rows)
+{
+    constexpr int kGroups = kUnitK / G;                       // of a unit
+    constexpr int kStageBytes = kUnitBytes + kGroups * 64;
+    constexpr int kPU = kXUnits / NB;                         // units of staged x
+    constexpr int kXStride = kPU * kUnitK * 2 + 16;           // 16: neighbouring rows in different banks
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int fw = kWarps / a.kparts, kpart = warp / fw, slot = warp % fw;
+    const int fwt = GATED ? fw / 2 : fw;                      // feature blocks of the block
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int b = tile * fwt + slot % fwt;
+    const bool on = b < a.blocks;
+    const uint8_t *base = GATED && slot >= fwt ? a.wv : a.w;
+    const size_t eb = static_cast<size_t>(e) * a.blocks + (on ? b : 0);
+    const uint8_t *wsrc = base + eb * a.units * kUnitBytes + lane * 16;
+    const uint8_t *ssrc = base + a.scales + eb * a.units * (kGroups * 64) + lane * 16;
+    const int u0 = static_cast<int>(static_cast<long>(a.units) * split / a.splits);
+    const int u1 = static_cast<int>(static_cast<long>(a.units) * (split + 1) / a.splits);
+
+    char *xs = smem + kWarps * kStages * kStageBytes;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+    const uint32_t xaddr = smem_u32(xs) + g * kXStride + c * 32;
+
+    float acc[2][NB][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
+
+    int next = u0 + kpart, put = 0;                           // next unit to copy, its stage
+    auto issue = [&]() {
+        if (on && next < u1) {
+            const uint32_t dst = ring + put * kStageBytes + lane * 16;
+            const uint8_t *s = wsrc + static_cast<size_t>(next) * kUnitBytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp16(dst + i * 512, s + i * 512);
+            if (lane < 4 * kGroups) cp16(dst + kUnitBytes, ssrc + static_cast<size_t>(next) * (kGroups * 64));
+        }
+        cp_commit();
+        next += a.kparts;
+        put = put + 1 == kStages ? 0 : put + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    int get = 0, u = u0 + kpart;                              // this warp's next unit
+    for (int p = u0; p < u1; p += kPU) {
+        const int pe = p + kPU < u1 ? p + kPU : u1;
+        __syncthreads();                                      // the last x is used up
+        stage_x(a, xs, kXStride, row0, rows, p * kUnitK, (pe - p) * kUnitK);
+        __syncthreads();
+        for (; u < pe; u += a.kparts) {
+            cp_wait<kStages - 2>();
+            __syncwarp();                                     // the scales are other lanes' copies; the last stage is read
+            issue();
+            const uint32_t st = ring + get * kStageBytes;
+            get = get + 1 == kStages ? 0 : get + 1;
+            if (!on) continue;
+            const uint32_t xu = xaddr + (u - p) * (kUnitK * 2);
+            float part[2][NB][4];
+            auto clear = [&]() {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[t][nb][i] = 0.f;
+            };
+            // the group's sums times its scales: features g, g + 8, g + 16, g + 24
+            auto flush = [&](int group) {
+                uint32_t lo, hi;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(st + kUnitBytes + group * 64 + g * 8));
+                const float s[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
+                                    __uint_as_float(hi & 0xffff0000u)};
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[t][nb][i] = fmaf(s[2 * t + (i >> 1)], part[t][nb][i], acc[t][nb][i]);
+            };
+            clear();
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                uint4 w[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) w[t] = lds128(st + (ch * 2 + t) * 512 + lane * 16);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {        // two steps of 16 inputs
+                    uint4 xv[NB];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) xv[nb] = lds128(xu + nb * (8 * kXStride) + ch * 128 + half * 16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t v = half ? (j ? w[t].w : w[t].z) : (j ? w[t].y : w[t].x);
+                            const uint32_t av[4] = {Deq<T>::template pair<0>(v), Deq<T>::template pair<1>(v),
+                                                    Deq<T>::template pair<2>(v), Deq<T>::template pair<3>(v)};
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                Deq<T>::mma(part[t][nb], av, j ? xv[nb].z : xv[nb].x, j ? xv[nb].w : xv[nb].y);
+                        }
+                    if (G == 32) {
+                        flush(ch * 2 + half);
+                        if (ch * 2 + half < 3) clear();
+                    }
+                }
+                if (G == 64) {
+                    flush(ch);
+                    if (ch == 0) clear();
+                }
+            }
+            if (G == 128) flush(0);
+        }
+    }
+
+    // Join: every warp leaves its sums [row][feature] in the ring's place; the cluster's blocks share
+    // the outputs and add the splits and warps in order.
+    cp_wait<0>();
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(smem);
+    constexpr int kWarpRed = NB * 8 * kRedStride;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[warp * kWarpRed + (nb * 8 + 2 * c + (i & 1)) * kRedStride + t * 16 + (i >> 1) * 8 + g] = acc[t][nb][i];
+    cg::cluster_group cl = cg::this_cluster();
+    if (a.splits > 1) cl.sync();
+    else __syncthreads();
+    const int width = fwt * kBlockF;
+    for (int i = split * (kWarps * 32) + threadIdx.x; i < rows * width; i += a.splits * (kWarps * 32)) {
+        const int n = i / width, f = i - n * width;           // width: a power of two times 32
+        const int feature = tile * width + f;
+        if (feature >= a.N) continue;
+        float v[2] = {0.f, 0.f};
+        for (int s = 0; s < a.splits; ++s) {
+            const float *src = a.splits > 1 ? cl.map_shared_rank(red, s) : red;
+            for (int kp = 0; kp < a.kparts; ++kp)
+#pragma unroll
+                for (int q = 0; q < (GATED ? 2 : 1); ++q)
+                    v[q] += src[(kp * fw + q * fwt + f / kBlockF) * kWarpRed + n * kRedStride + f % kBlockF];
+        }
+        const float y = GATED ? gelu_of(v[0]) * v[1] : v[0];
+        const size_t at = static_cast<size_t>(row0 + n) * a.N + feature;
+        if (a.out_f32) static_cast<float *>(a.y)[at] = y;
+        else static_cast<T *>(a.y)[at] = from_f32<T>(y);
+    }
+    // no block overwrites its sums, or ends, while another reads them
+    if (a.splits > 1) cl.sync();
+    else __syncthreads();
+}
+
+template <class T, int G, bool GATED>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
+{
+    extern __shared__ __align__(16) char w4_smem[];
+    const int e = blockIdx.y;
+    int r0 = 0, r1 = a.R;
+    if (a.offsets) {
+        r0 = max(__ldg(a.offsets + e), 0);
+        r1 = min(__ldg(a.offsets + e + 1), a.R);
+    }
+    // all blocks of a cluster have the same expert: they leave, and pass, together
+    for (; r0 < r1; r0 += 32) {
+        const int rows = min(r1 - r0, 32);
+        if (rows <= 8) w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
+        else if (rows <= 16) w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
+        else w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
+    }
+}
+
+constexpr int smem_bytes(int G)
+{
+    return kWarps * kStages * (kUnitBytes + kUnitK / G * 64) + 8 * (kXUnits * kUnitK * 2 + 16) + 4 * 8 * 16;
+}
+
+template <class T, int G, bool GATED>
+cudaError_t launch_w4(W4Args a, cudaStream_t s)
+{
+    constexpr int smem = smem_bytes(G);
+    static_assert(smem >= kWarps * 4 * 8 * kRedStride * 4, "the partial sums take the ring's place");
+    const cudaError_t e =
+        cudaFuncSetAttribute(w4_kernel<T, G, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
+    }
+    // Warps on the inputs and blocks on the inputs: the fewest rounds of the SMs' two blocks, counted
+    // in units a warp walks, with half a unit for each round's start and end.  At most as many experts
+    // have work as there are rows.
+    const int busy = a.offsets && a.R < a.E ? a.R : a.E;
+    double best = 0;
+    for (int kp = 1; kp <= (GATED ? 4 : 8); kp *= 2) {
+        const int fwt = kWarps / kp / (GATED ? 2 : 1);
+        const long tiles = static_cast<long>((a.blocks + fwt - 1) / fwt) * busy;
+        for (int sp = 1; sp <= 8; ++sp) {
+            if (sp > 1 && sp * kp > a.units) break;
+            const long rounds = (tiles * sp + 2 * kSms - 1) / (2 * kSms);
+            const int walk = ((a.units + sp - 1) / sp + kp - 1) / kp;
+            const double cost = rounds * (walk + 4.0) + 0.1 * sp;
+            if (best == 0 || cost < best) {
+                best = cost;
+                a.splits = sp;
+                a.kparts = kp;
+            }
+        }
+    }
+    const int fwt = kWarps / a.kparts / (GATED ? 2 : 1);
+    const dim3 grid(static_cast<unsigned>((a.blocks + fwt - 1) / fwt * a.splits), a.E);
+    return op_launch(w4_kernel<T, G, GATED>, grid, dim3(kWarps * 32), smem, s, false, a.splits, a);
+}
+
+template <class T>
+cudaError_t w4_by_group(int G, const W4Args &a, cudaStream_t s)
+{
+    if (a.wv) return G == 32 ? launch_w4<T, 32, true>(a, s) : G == 64 ? launch_w4<T, 64, true>(a, s) : launch_w4<T, 128, true>(a, s);
+    return G == 32 ? launch_w4<T, 32, false>(a, s) : G == 64 ? launch_w4<T, 64, false>(a, s) : launch_w4<T, 128, false>(a, s);
+}
+
+int w4_sizes(int E, int K, int N, int G)
+{
+    if (E < 1 || K < 1 || N < 1 || K > 131072 || N > 131072) return MOE_EINVAL;
+    if (E > kMaxWExperts || (G != 32 && G != 64 && G != 128)) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" MOE_API long long moe_w4_packed_bytes(int E, int K, int N, int group)
+{
+    const int rc = w4_sizes(E, K, N, group);
+    return rc != MOE_OK ? rc : static_cast<long long>(shape_of(E, K, N, group).bytes);
+}
+
+extern "C" MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t *q, const void *scales, void *packed,
+                                   void *stream)
+{
+    int rc = w4_sizes(E, K, N, group);
+    if (rc != MOE_OK) return rc;
+    if (!op_ptr(q) || !op_ptr(scales) || !op_ptr(packed)) return MOE_EINVAL;
+    const W4Shape sh = shape_of(E, K, N, group);
+    if (op_overlap(q, static_cast<size_t>(E) * K * N, packed, sh.bytes) ||
+        op_overlap(scales, static_cast<size_t>(E) * ((K + group - 1) / group) * N * 2, packed, sh.bytes))
+        return MOE_EINVAL;
+    if ((rc = op_device()) != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *out = static_cast<uint8_t *>(packed);
+    int *flag = reinterpret_cast<int *>(out + sh.bytes - kTail);
+    const size_t words = sh.scales / 4, nscales = (sh.bytes - kTail - sh.scales) / 2;
+    int bad = 0;
+    if (cudaMemsetAsync(flag, 0, kTail, s) != cudaSuccess ||
+        op_launch(w4_pack_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, false, 1, sh, q,
+                  reinterpret_cast<uint32_t *>(out), flag) != cudaSuccess ||
+        op_launch(w4_pack_scales_kernel, dim3(static_cast<unsigned>((nscales + 255) / 256)), dim3(256), 0, s, false, 1, sh,
+                  static_cast<const __nv_bfloat16 *>(scales), reinterpret_cast<__nv_bfloat16 *>(out + sh.scales)) !=
+            cudaSuccess ||
+        cudaMemcpyAsync(&bad, flag, sizeof bad, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ECUDA;
+    }
+    return bad ? MOE_ERANGE : MOE_OK;
+}
+
+extern "C" MOE_API int moe_w4_matvec(int dtype, int out_dtype, int E, int K, int N, int group, int R, const void *x,
+                                     const int32_t *offsets, const void *packed, const void *packed_v, void *y,
+                                     void *stream)
+{
+    int rc = w4_sizes(E, K, N, group);
+    if (rc != MOE_OK) return rc;
+    if (!dtype_known(dtype) || !dtype_known(out_dtype) || R < 0) return MOE_EINVAL;
+    if (dtype == MOE_F32 || (out_dtype != dtype && out_dtype != MOE_F32) || R > kMaxRows) return MOE_EUNSUPPORTED;
+    if (R == 0) return MOE_OK;
+    if (!op_ptr(x) || !op_ptr(packed) || !op_ptr(y) || !op_aligned16(offsets) || !op_aligned16(packed_v)) return MOE_EINVAL;
+    if (!offsets && E != 1) return MOE_EINVAL;
+    const W4Shape sh = shape_of(E, K, N, group);
+    const size_t yb = static_cast<size_t>(R) * N * dtype_size(out_dtype);
+    if (op_overlap(x, static_cast<size_t>(R) * K * 2, y, yb) || op_overlap(packed, sh.bytes, y, yb) ||
+        op_overlap(packed_v, sh.bytes, y, yb) || op_overlap(offsets, (static_cast<size_t>(E) + 1) * 4, y, yb))
+        return MOE_EINVAL;
+    if ((rc = op_device()) != MOE_OK) return rc;
+    const W4Args a{E, K, N, R, sh.blocks, sh.units, sh.scales, x, offsets, static_cast<const uint8_t *>(packed),
+                   static_cast<const uint8_t *>(packed_v), y, out_dtype == MOE_F32, 1, 1};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return (dtype == MOE_BF16 ? w4_by_group<__nv_bfloat16>(group, a, s) : w4_by_group<__half>(group, a, s)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
+}

@@ -119,3 +119,36 @@ def norm_grad(x, gain, stats, dy, layer, dtype):
     n = math.ceil(T / 64) + 100
     dgain, dbias = (dy * xh).sum(0), dy.sum(0)
     return (dx, dgain, dbias), (tol, n * U * (dy * xh).abs().sum(0) + 1e-44, n * U * dy.abs().sum(0) + 1e-44)
+
+
+def w4(x, offsets, packs, group, dtype):
+    """x [R, K], packs = [(q [E, K, N], s [E, groups, N])] (two: gated) -> y (nan in rows of no expert), bound.
+
+    A multiply step adds 16 exact products and the running sum, each cut at the place of the largest: at most
+    17 * 2 U of the group's sizes a step; then one rounding a group, and at most 40 joins."""
+    R, K = x.shape
+    N = packs[0][0].shape[2]
+    y = torch.full((R, N), math.nan, dtype=F8)
+    tol = torch.zeros_like(y)
+    count = 34 * group / 16 + 2 * math.ceil(K / group) + 40
+    for e in range(len(offsets) - 1):
+        r0, r1 = max(int(offsets[e]), 0), min(int(offsets[e + 1]), R)
+        if r0 >= r1:
+            continue
+        xe = x[r0:r1].to(F8)
+        v, dv = [], []
+        for q, s in packs:
+            w = q[e].to(F8) * s[e].to(F8).repeat_interleave(group, 0)[:K]
+            v.append(xe @ w)
+            dv.append(count * U * (xe.abs() @ w.abs()))
+        if len(packs) == 1:
+            y[r0:r1], tol[r0:r1] = v[0], dv[0]
+            continue
+        a, da = v[0], dv[0]
+        z = math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)
+        gelu = a / (1 + torch.exp(-2 * z))
+        y[r0:r1] = gelu * v[1]
+        # |gelu'| <= 1.13; z's few roundings come back 2 |z| times larger from the exponential
+        tol[r0:r1] = (1.13 * da * (v[1].abs() + dv[1]) + gelu.abs() * dv[1]
+                      + (8 * z.abs() + 8) * U * (gelu * v[1]).abs())
+    return y, tol + half_ulp(y, dtype).nan_to_num(0.0) + 1e-44

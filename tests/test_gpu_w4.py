@@ -1,0 +1,183 @@
+"""Few rows times 4-bit expert weights (moe_w4_pack, moe_w4_matvec) against the plain 64-bit form: both input types
+and output types, all group sizes, one row to several passes, shapes that do not fill a block or a unit,
+inputs split over warps and clusters, experts without rows; and the operators together as a layer."""
+import math
+
+import pytest
+import torch
+
+from tests import ops64
+from tests.test_gpu_rows import DT, guarded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_softmax_b200 as m
+    return m
+
+
+def weights(E, K, N, group, seed):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(-8, 8, (E, K, N), generator=g, dtype=torch.int8)
+    s = (torch.randn((E, -(-K // group), N), generator=g) / (4 * math.sqrt(K))).to(torch.bfloat16)
+    return q, s
+
+
+def pack(m, q, s, group):
+    E, K, N = q.shape
+    p, check = guarded((m.moe_w4_packed_bytes(E, K, N, group),), torch.uint8, 77)
+    m.check(m.moe_w4_pack(E, K, N, group, q.cuda(), s.cuda(), p), "moe_w4_pack")
+    check()
+    return p
+
+
+def run(m, dt, out, x, offsets, packs, group, shape):
+    E, K, N = shape
+    R = x.shape[0]
+    y, check = guarded((R, N), DT[out], 99.0)
+    p = [pack(m, q, s, group) for q, s in packs] + [None]
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    m.check(m.moe_w4_matvec(dt, out, E, K, N, group, R, x.cuda(), off, p[0], p[1], y), "moe_w4_matvec")
+    torch.cuda.synchronize()
+    check()
+    return y.cpu()
+
+
+def check_rows(got, ref, tol):
+    hit = ~ref.isnan().all(1)
+    ops64.assert_close(got[hit], ref[hit], tol[hit], "y")
+    assert (got[~hit] == 99.0).all(), "a row of no expert changed"
+
+
+# (R, K, N): blocks and units that are not full, one unit, many splits, every operand count, several passes
+SHAPES = [(1, 1, 1), (1, 128, 32), (1, 127, 31), (2, 6144, 512), (3, 333, 77), (7, 64, 4100), (8, 4096, 96), (9, 257, 64),
+          (16, 1000, 200), (17, 2048, 40), (31, 130, 260), (32, 512, 128), (33, 384, 96), (70, 264, 50), (1, 20000, 33)]
+
+
+@pytest.mark.parametrize("R,K,N", SHAPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt,out", [(0, 0), (1, 1), (0, 2), (1, 2)])
+def test_matvec(m, R, K, N, group, dt, out):
+    pk = weights(1, K, N, group, K + N)
+    x = torch.randn((R, K), generator=torch.Generator().manual_seed(R)).to(DT[dt])
+    ref, tol = ops64.w4(x, [0, R], [pk], group, DT[out])
+    check_rows(run(m, dt, out, x, None, [pk], group, (1, K, N)), ref, tol)
+
+
+@pytest.mark.parametrize("R,K,N", [(1, 128, 32), (2, 333, 77), (8, 2048, 520), (12, 130, 100), (40, 512, 64), (5, 9000, 48)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_gated(m, R, K, N, group, dt):
+    packs = [weights(1, K, N, group, s) for s in (1, 2)]
+    x = torch.randn((R, K), generator=torch.Generator().manual_seed(R)).to(DT[dt])
+    ref, tol = ops64.w4(x, [0, R], packs, group, DT[dt])
+    check_rows(run(m, dt, dt, x, None, packs, group, (1, K, N)), ref, tol)
+
+
+OFFSETS = {"spread": [0, 2, 3, 9, 10], "empty": [0, 0, 5, 5, 10], "one": [0, 0, 0, 10, 10], "none": [0, 0, 0, 0, 0],
+           "tail": [0, 1, 2, 3, 4], "behind": [2, 4, 4, 6, 8], "long": [0, 1, 34, 40, 40]}
+
+
+@pytest.mark.parametrize("name", sorted(OFFSETS))
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("group,K,N", [(128, 520, 72), (32, 2048, 256)])
+def test_experts(m, name, gated, group, K, N):
+    offsets = OFFSETS[name]
+    R = max(10, offsets[-1] + (2 if name == "tail" else 0))
+    packs = [weights(4, K, N, group, s) for s in range(2 if gated else 1)]
+    x = torch.randn((R, K), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    ref, tol = ops64.w4(x, offsets, packs, group, torch.float32)
+    check_rows(run(m, 0, 2, x, offsets, packs, group, (4, K, N)), ref, tol)
+
+
+def test_offsets_are_clamped(m):
+    """Row ranges outside [0, R] lose what lies outside; nothing is read or written there."""
+    pk = weights(3, 256, 64, 64, 0)
+    x = torch.randn((6, 256), generator=torch.Generator().manual_seed(0)).to(torch.float16)
+    offsets = [-3, 2, 1, 2 ** 31 - 1]
+    got = run(m, 1, 2, x, offsets, [pk], 64, (3, 256, 64))
+    # row 1 lies in the ranges of experts 0 and 2: it gets either one's product, the others have one
+    ref, tol = ops64.w4(x, offsets, [pk], 64, torch.float32)
+    first, ftol = ops64.w4(x, [0, 2, 2, 2], [pk], 64, torch.float32)
+    last = ((got[1].double() - ref[1]).abs() <= tol[1]).all()
+    assert last or ((got[1].double() - first[1]).abs() <= ftol[1]).all()
+    rest = [0, 2, 3, 4, 5]
+    check_rows(got[rest], ref[rest], tol[rest])
+
+
+def test_every_value_and_place(m):
+    """Each weight of a small matrix is found again, exactly, by unit rows; values cover -8 .. 7."""
+    for group, K, N in ((32, 160, 40), (64, 192, 33), (128, 129, 64)):
+        q = (torch.arange(K * N).view(1, K, N) * 7 % 16 - 8).to(torch.int8)
+        s = (1 + torch.arange(-(-K // group) * N).view(1, -1, N) % 128).to(torch.bfloat16)
+        want = q[0].float() * s[0].float().repeat_interleave(group, 0)[:K]
+        for at in range(0, K, 32):
+            x = torch.zeros((min(32, K - at), K), dtype=torch.bfloat16)
+            x[torch.arange(x.shape[0]), at + torch.arange(x.shape[0])] = 1
+            got = run(m, 0, 2, x, None, [(q, s)], group, (1, K, N))
+            assert torch.equal(got, want[at:at + 32])
+
+
+def test_values_outside_the_range_are_refused(m):
+    for bad in (-9, 8, 127, -128):
+        q = torch.zeros((2, 40, 24), dtype=torch.int8)
+        q[1, 39, 23] = bad
+        s = torch.ones((2, 2, 24), dtype=torch.bfloat16)
+        p = torch.empty(m.moe_w4_packed_bytes(2, 40, 24, 32), dtype=torch.uint8, device="cuda")
+        assert m.moe_w4_pack(2, 40, 24, 32, q.cuda(), s.cuda(), p) == m.MOE_ERANGE
+        q[1, 39, 23] = max(-8, min(7, bad))
+        assert m.moe_w4_pack(2, 40, 24, 32, q.cuda(), s.cuda(), p) == m.MOE_OK
+
+
+def test_nonfinite_inputs_stay_in_their_row(m):
+    pk = weights(1, 300, 48, 64, 3)
+    x = torch.randn((5, 300), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    clean, tol = ops64.w4(x, [0, 5], [pk], 64, torch.float32)
+    x[1, 299] = float("nan")
+    x[3, 0] = float("inf")
+    got = run(m, 0, 2, x, None, [pk], 64, (1, 300, 48))
+    keep = [0, 2, 4]
+    ops64.assert_close(got[keep], clean[keep], tol[keep])
+    assert got[1].isnan().all()
+    # inf times a weight of 0 is nan, times any other an infinity of its sign
+    w = pk[0][0, 0].double() * pk[1][0, 0].double()
+    assert got[3][w == 0].isnan().all() and torch.equal(got[3][w != 0].double(), torch.sign(w[w != 0]) * math.inf)
+
+
+def test_large_values(m):
+    """fp16 inputs near the type's largest value: the sums are fp32."""
+    pk = weights(1, 512, 64, 128, 8)
+    x = torch.full((4, 512), 60000.0).to(torch.float16)
+    x[::2] *= -1
+    ref, tol = ops64.w4(x, [0, 4], [pk], 128, torch.float32)
+    check_rows(run(m, 1, 2, x, None, [pk], 128, (1, 512, 64)), ref, tol)
+
+
+def test_same_bits_every_time(m):
+    pk = weights(8, 1024, 512, 64, 1)
+    x = torch.randn((24, 1024), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    offsets = [0, 3, 3, 10, 11, 12, 20, 23, 24]
+    a = run(m, 0, 2, x, offsets, [pk], 64, (8, 1024, 512))
+    for _ in range(3):
+        assert torch.equal(a, run(m, 0, 2, x, offsets, [pk], 64, (8, 1024, 512)))
+
+
+def test_weights_beyond_2_gib(m):
+    """Experts whose packed weights lie behind 2^31 bytes: 24 experts of 16384 x 12288 (2.4 GB)."""
+    E, K, N, group = 24, 16384, 12288, 128
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randint(-8, 8, (1, K, N), generator=g, device="cuda", dtype=torch.int8)
+    p = torch.zeros(m.moe_w4_packed_bytes(E, K, N, group), dtype=torch.uint8, device="cuda")
+    s = torch.full((1, K // group, N), 2.0 ** -6, dtype=torch.bfloat16, device="cuda")
+    full_q = q.expand(E, K, N).contiguous()
+    full_q[:E - 1] = 0
+    m.check(m.moe_w4_pack(E, K, N, group, full_q, s.expand(E, -1, -1).contiguous(), p))
+    del full_q
+    x = torch.randint(-4, 5, (3, K), generator=g, device="cuda").to(torch.bfloat16)
+    offsets = torch.tensor([0] * E + [3], dtype=torch.int32, device="cuda")
+    y = torch.full((3, N), 99.0, device="cuda")
+    m.check(m.moe_w4_matvec(m.MOE_BF16, m.MOE_F32, E, K, N, group, 3, x, offsets, p, None, y))
+    want = (x.double() @ q[0].double()) * 2.0 ** -6    # whole numbers below 2^24: exact in fp32
+    assert torch.equal(y.double(), want)

@@ -116,3 +116,30 @@ def test_tensor_arguments_are_checked(m):
         m.moe_norm_forward(m.MOE_NORM_RMS, m.MOE_BF16, 4, 64, x, None, None, 1e-5, x, None, 0)   # not on the GPU
     with pytest.raises(TypeError):
         m.moe_norm_forward(m.MOE_NORM_RMS, m.MOE_BF16, 4, 64, [1.0], None, None, 1e-5, x, None, 0)
+
+
+def test_w4_refusals(m, ran):
+    assert m.moe_w4_packed_bytes(0, 64, 64, 32) == m.MOE_EINVAL
+    assert m.moe_w4_packed_bytes(1, 0, 64, 32) == m.MOE_EINVAL
+    assert m.moe_w4_packed_bytes(1, 64, 131073, 32) == m.MOE_EINVAL
+    assert m.moe_w4_packed_bytes(1, 64, 64, 48) == m.MOE_EUNSUPPORTED
+    assert m.moe_w4_packed_bytes(1025, 64, 64, 32) == m.MOE_EUNSUPPORTED
+    # half a byte a weight, two bytes a group's scale, and a tail
+    assert m.moe_w4_packed_bytes(8, 6144, 32768, 128) - 8 * (6144 * 32768 // 2 + 48 * 32768 * 2) in range(0, 4096)
+    good = dict(E=2, K=64, N=64, group=32, q=addr(0), scales=addr(1), packed=addr(2), stream=0)
+    check_refusals(m.moe_w4_pack, good, ran, [("E", 0), ("K", 0), ("N", 0), ("packed", addr(0)), ("packed", addr(1) + 16)],
+                   ["q", "scales", "packed"])
+    assert m.moe_w4_pack(**{**good, "group": 256}) == m.MOE_EUNSUPPORTED
+
+
+def test_w4_matvec_refusals(m, ran):
+    good = dict(dtype=m.MOE_BF16, out_dtype=m.MOE_F32, E=2, K=64, N=64, group=32, R=3, x=addr(0), offsets=addr(1), packed=addr(2),
+                packed_v=addr(3), y=addr(4), stream=0)
+    check_refusals(m.moe_w4_matvec, good, ran,
+                   [("dtype", 7), ("out_dtype", 7), ("E", 0), ("K", 0), ("N", 0), ("K", 131073), ("R", -1), ("y", addr(0)),
+                    ("y", addr(1)), ("y", addr(2) + 16), ("y", addr(3)), ("offsets", None)],
+                   ["x", "offsets", "packed", "packed_v", "y"], optional=("packed_v",))
+    for name, bad in (("dtype", m.MOE_F32), ("out_dtype", m.MOE_F16), ("group", 16), ("R", 1025), ("E", 1025)):
+        assert m.moe_w4_matvec(**{**good, name: bad}) == m.MOE_EUNSUPPORTED, name
+    assert m.moe_w4_matvec(**{**good, "E": 1, "offsets": None, "packed_v": None}) in ran
+    assert m.moe_w4_matvec(**{**good, "R": 0, "x": None}) == m.MOE_OK
