@@ -13,6 +13,7 @@ a non-zero status into ``MoEError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -300,42 +301,54 @@ def moe_ep_combine(h, T, y_back, out, stream=None) -> int:
 # be what the C side reads: dense, on the current CUDA device, of the named element type and at
 # least as long as the call's sizes say; anything else raises ValueError.  Integers are raw addresses.
 
-_DTYPES = None
+_torch = None     # torch's element types by code, and its current device and stream
 
 
-def _dtype_of(code):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {MOE_BF16: torch.bfloat16, MOE_F16: torch.float16, MOE_F32: torch.float32,
-                   "i32": torch.int32, "i8": torch.int8, "u8": torch.uint8}
-    return _DTYPES.get(code)
+def _torch_side():
+    global _torch
+    import torch
+    kinds = {MOE_BF16: torch.bfloat16, MOE_F16: torch.float16, MOE_F32: torch.float32,
+             "i32": torch.int32, "i8": torch.int8, "u8": torch.uint8}
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = (kinds, torch.cuda.current_device, raw)
+    return _torch
+
+
+def _op_stream(stream):
+    """stream, or the current one of the current device (the short way: small calls last a few microseconds)."""
+    if stream is not None:
+        return _stream(stream)
+    _, device, raw = _torch or _torch_side()
+    return raw(device()) if raw else _stream(None)
 
 
 def _arg(t, name, code, numel):
     """Address of one operand.  code: its element type; numel: the elements that the call may touch."""
     if t is None or isinstance(t, int):
         return t
-    if not hasattr(t, "data_ptr"):
-        raise TypeError(f"{name}: cannot pass {type(t).__name__} as a pointer")
+    kinds, device, _ = _torch or _torch_side()
+    want = kinds.get(code)
+    try:
+        if t.dtype is want and t.is_cuda and t.is_contiguous() and t.numel() >= numel and t.get_device() == device():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name}: cannot pass {type(t).__name__} as a pointer") from None
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: needs a dense CUDA tensor")
-    want = _dtype_of(code)
     if want is not None and t.dtype is not want:
         raise ValueError(f"{name}: {t.dtype}, needs {want}")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, needs {numel}")
-    import torch
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != device():
         raise ValueError(f"{name}: on {t.device}, which is not the current device")
-    return t.data_ptr()
+    return t.data_ptr()   # an unknown type code: the C side refuses it
 
 
 def moe_sort_rows(dtype, T, k, E, d, x, idx, offsets, perm, slot, rows, stream=None) -> int:
     n = T * k
     return _lib.moe_sort_rows(dtype, T, k, E, d, _arg(x, "x", dtype, T * d), _arg(idx, "idx", "i32", n),
                               _arg(offsets, "offsets", "i32", E + 1), _arg(perm, "perm", "i32", n),
-                              _arg(slot, "slot", "i32", n), _arg(rows, "rows", dtype, n * d), _stream(stream))
+                              _arg(slot, "slot", "i32", n), _arg(rows, "rows", dtype, n * d), _op_stream(stream))
 
 
 def moe_unsort_rows(rows_dtype, dtype, T, k, d, rows, slot, gate, out, stream=None) -> int:
@@ -343,7 +356,7 @@ def moe_unsort_rows(rows_dtype, dtype, T, k, d, rows, slot, gate, out, stream=No
     n = T * k
     return _lib.moe_unsort_rows(rows_dtype, dtype, T, k, d, _arg(rows, "rows", rows_dtype, n * d),
                                 _arg(slot, "slot", "i32", n), _arg(gate, "gate", MOE_F32, n),
-                                _arg(out, "out", dtype, T * d), _stream(stream))
+                                _arg(out, "out", dtype, T * d), _op_stream(stream))
 
 
 def moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, dout, rows, slot, gate, drows, dgate, stream=None) -> int:
@@ -351,13 +364,13 @@ def moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, dout, rows, slot, gate,
     return _lib.moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, _arg(dout, "dout", dtype, T * d),
                                          _arg(rows, "rows", rows_dtype, n * d), _arg(slot, "slot", "i32", n),
                                          _arg(gate, "gate", MOE_F32, n), _arg(drows, "drows", rows_dtype, n * d),
-                                         _arg(dgate, "dgate", MOE_F32, n), _stream(stream))
+                                         _arg(dgate, "dgate", MOE_F32, n), _op_stream(stream))
 
 
 def moe_norm_forward(kind, dtype, T, d, x, gain, bias, eps, y, stats=None, stream=None) -> int:
     return _lib.moe_norm_forward(kind, dtype, T, d, _arg(x, "x", dtype, T * d), _arg(gain, "gain", dtype, d),
                                  _arg(bias, "bias", dtype, d), eps, _arg(y, "y", dtype, T * d),
-                                 _arg(stats, "stats", MOE_F32, 2 * T), _stream(stream))
+                                 _arg(stats, "stats", MOE_F32, 2 * T), _op_stream(stream))
 
 
 def moe_norm_backward(kind, dtype, T, d, x, gain, stats, dy, dx, dgain, dbias, workspace, stream=None) -> int:
@@ -365,14 +378,16 @@ def moe_norm_backward(kind, dtype, T, d, x, gain, stats, dy, dx, dgain, dbias, w
                                   _arg(stats, "stats", MOE_F32, 2 * T), _arg(dy, "dy", dtype, T * d),
                                   _arg(dx, "dx", dtype, T * d), _arg(dgain, "dgain", MOE_F32, d),
                                   _arg(dbias, "dbias", MOE_F32, d),
-                                  _arg(workspace, "workspace", "u8", moe_norm_workspace(T, d)), _stream(stream))
+                                  _arg(workspace, "workspace", "u8", moe_norm_workspace(T, d)), _op_stream(stream))
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_norm_workspace(T, d) -> int:
     """Bytes (a uint8 tensor's length) of moe_norm_backward's workspace, or a negative status."""
     return _lib.moe_norm_workspace(T, d)
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_w4_packed_bytes(E, K, N, group) -> int:
     """Bytes (a uint8 tensor's length) of packed 4-bit weights, or a negative status."""
     return _lib.moe_w4_packed_bytes(E, K, N, group)
@@ -382,14 +397,14 @@ def moe_w4_pack(E, K, N, group, q, scales, packed, stream=None) -> int:
     """q int8 [E, K, N] in [-8, 7], scales bf16 [E, ceil(K / group), N] -> packed uint8."""
     return _lib.moe_w4_pack(E, K, N, group, _arg(q, "q", "i8", E * K * N),
                             _arg(scales, "scales", MOE_BF16, E * -(-K // max(group, 1)) * N),
-                            _arg(packed, "packed", "u8", moe_w4_packed_bytes(E, K, N, group)), _stream(stream))
+                            _arg(packed, "packed", "u8", moe_w4_packed_bytes(E, K, N, group)), _op_stream(stream))
 
 
 def moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, x, offsets, packed, packed_v, y, stream=None) -> int:
     nbytes = moe_w4_packed_bytes(E, K, N, group)
     return _lib.moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, _arg(x, "x", dtype, R * K),
                               _arg(offsets, "offsets", "i32", E + 1), _arg(packed, "packed", "u8", nbytes),
-                              _arg(packed_v, "packed_v", "u8", nbytes), _arg(y, "y", out_dtype, R * N), _stream(stream))
+                              _arg(packed_v, "packed_v", "u8", nbytes), _arg(y, "y", out_dtype, R * N), _op_stream(stream))
 
 
 def moe_plan(h, T: int):
