@@ -5,13 +5,17 @@
 //   dx = r (h - mean(h) - xh mean(h xh)),   h = dy g,  xh = (x - m) r   (no mean(h) for RMSNorm)
 //   dg = sum over rows of dy xh,   db = sum over rows of dy
 //
-// Both directions are bound by memory traffic (forward: x in, y out; backward: x and dy in, dx out).
-// A row is held in registers from its load to its store, so it is read once: by one warp where
-// it fits into the lanes' registers, else by a block.  The variance is taken around the mean, not as
-// a difference of squares.  The backward pass runs a fixed number of blocks that walk over the rows
+// Both directions are bound by memory traffic (forward: x in, y out; backward: x and dy in, dx out);
+// a row is read once and held until its result is written: in registers, or in a ring of shared memory
+// that asynchronous copies fill some rows ahead.  The variance is taken around the mean, not as a
+// difference of squares.  The backward pass runs a fixed number of blocks that walk over the rows
 // and keep the columns' sums of dg and db in registers; each block leaves one row of partial sums
 // and a second, short kernel adds those in block order, so results do not depend on scheduling.
-// Rows too wide for the registers are read again from the caches instead, and their columns' sums
+//
+// Rows whose width is no multiple of 16 bytes still move in 16-byte vectors: rows r, r + P, r + 2 P ...
+// (P = 16 bytes over their common divisor with the row) begin at the same place within a vector,
+// so a block that takes rows of one such class has its columns at fixed places.
+// Rows too wide for a block are read again from the caches instead, and their columns' sums
 // taken by a kernel of their own.
 #include "ops_common.cuh"
 
@@ -45,95 +49,354 @@ __device__ __forceinline__ float row_sum(float v, float *buf)
     return warp_sum(lane < (static_cast<int>(blockDim.x) >> 5) ? buf[lane] : 0.f);
 }
 
-template <class T, int N, int NV, bool LAYER, bool WARP>
+template <class T>
+__device__ __forceinline__ Vec<T, 16 / sizeof(T)> as_vec(uint4 u)
+{
+    Vec<T, 16 / sizeof(T)> r;
+    memcpy(r.v, &u, 16);
+    return r;
+}
+
+// where the vectors of a row are: column c of a row is element c + shift of the vectors that hold it
+template <class T>
+struct Place {
+    static constexpr int W = 16 / sizeof(T);
+    int d, shift, nv;           // nv: vectors that hold a row
+    // the first vector may begin with the row before's end, the last may end behind this row
+    __device__ __forceinline__ bool inner(int v) const { return v * W >= shift && (v + 1) * W <= shift + d; }
+    __device__ __forceinline__ bool has(int v, int e) const { return v * W + e >= shift && v * W + e < shift + d; }
+    __device__ __forceinline__ int bytes(int v) const
+    {
+        const int n = (shift + d - v * W) * static_cast<int>(sizeof(T));
+        return n < 16 ? n : 16;
+    }
+    // the bits of vector v that are this row's
+    __device__ __forceinline__ uint4 keep(int v) const
+    {
+        uint32_t m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            m[j] = W == 4 ? (has(v, j) ? 0xffffffffu : 0u)
+                          : (has(v, 2 * j) ? 0xffffu : 0u) | (has(v, 2 * j + 1) ? 0xffff0000u : 0u);
+        return make_uint4(m[0], m[1], m[2], m[3]);
+    }
+    // vector v of a row whose first vector is at p; elements outside the row are 0 (and not read)
+    __device__ __forceinline__ uint4 load(const T *p, int v) const
+    {
+        if (inner(v)) return __ldg(reinterpret_cast<const uint4 *>(p + v * W));
+        Vec<T, W> r;
+#pragma unroll
+        for (int e = 0; e < W; ++e) r.v[e] = has(v, e) ? p[v * W + e] : from_f32<T>(0.f);
+        uint4 u;
+        memcpy(&u, r.v, 16);
+        return u;
+    }
+    __device__ __forceinline__ void store(T *p, int v, const Vec<T, W> &o) const
+    {
+        if (inner(v)) {
+            st_vec<T, W>(p + v * W, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (has(v, e)) p[v * W + e] = o.v[e];
+        }
+    }
+};
+
+__device__ __forceinline__ uint4 bits_and(uint4 a, uint4 k) { return make_uint4(a.x & k.x, a.y & k.y, a.z & k.z, a.w & k.w); }
+
+// sum of a pair's halves
+__device__ __forceinline__ float both(F2 a)
+{
+    const float2 f = unpack(a);
+    return f.x + f.y;
+}
+
+// rows of whole vectors, held in registers
+template <class T, int NV, bool LAYER, bool WARP>
 __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) norm_kernel(NormArgs a)
 {
+    constexpr int W = 16 / sizeof(T);
     __shared__ float buf[2][32];
-    const int nt = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x, nv = a.d / W;
     const int row = WARP ? blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= a.T) return;
-    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.d;
-    Vec<T, N> v[NV];
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.d) + tid;
+    uint4 u[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((i * nt + tid) * N < a.d) v[i] = ld_vec<T, N>(x + (i * nt + tid) * N);
+        if (i * nt + tid < nv) u[i] = __ldg(x + i * nt);
+    const float inv = 1.f / static_cast<float>(a.d);
     float mean = 0.f;
     if constexpr (LAYER) {
-        float s = 0.f;
+        F2 s = f2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((i * nt + tid) * N < a.d) {
+            if (i * nt + tid < nv) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) s += to_f32(v[i].v[e]);
+                for (int e = 0; e < W / 2; ++e) s = add2(s, pair_of<T>(u[i], e));
             }
-        mean = row_sum<WARP>(s, buf[0]) / static_cast<float>(a.d);
+        mean = row_sum<WARP>(both(s), buf[0]) * inv;
     }
-    float q = 0.f;
+    const F2 nm = f2(-mean, -mean);
+    F2 q = f2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((i * nt + tid) * N < a.d) {
+        if (i * nt + tid < nv) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float c = to_f32(v[i].v[e]) - mean;
-                q = fmaf(c, c, q);
+            for (int e = 0; e < W / 2; ++e) {
+                F2 c = pair_of<T>(u[i], e);
+                if constexpr (LAYER) c = add2(c, nm);
+                q = fma2(c, c, q);
             }
         }
-    const float r = 1.f / sqrtf(row_sum<WARP>(q, buf[1]) / static_cast<float>(a.d) + a.eps);
+    const float r = 1.f / sqrtf(row_sum<WARP>(both(q), buf[1]) * inv + a.eps);
     if (tid == 0 && a.stats) *reinterpret_cast<float2 *>(a.stats + 2 * static_cast<size_t>(row)) = make_float2(mean, r);
+    const F2 rr = f2(r, r);
     T *y = static_cast<T *>(a.y) + static_cast<size_t>(row) * a.d;
-    const T *gain = static_cast<const T *>(a.gain), *bias = static_cast<const T *>(a.bias);
+    const uint4 *gain = static_cast<const uint4 *>(a.gain), *bias = static_cast<const uint4 *>(a.bias);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * nt + tid) * N;
-        if (c >= a.d) continue;
-        Vec<T, N> g, b, o;
-        if (gain) g = ld_vec<T, N>(gain + c);
-        if (LAYER && bias) b = ld_vec<T, N>(bias + c);
+        const int v = i * nt + tid;
+        if (v >= nv) continue;
+        uint4 g, b;
+        if (gain) g = __ldg(gain + v);
+        if (LAYER && bias) b = __ldg(bias + v);
+        Vec<T, W> o;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float h = (to_f32(v[i].v[e]) - mean) * r;
-            if (gain) h *= to_f32(g.v[e]);
-            if (LAYER && bias) h += to_f32(b.v[e]);
-            o.v[e] = from_f32<T>(h);
+        for (int e = 0; e < W / 2; ++e) {
+            F2 h = pair_of<T>(u[i], e);
+            if constexpr (LAYER) h = add2(h, nm);
+            h = mul2(h, rr);
+            if (LAYER && bias) h = gain ? fma2(h, pair_of<T>(g, e), pair_of<T>(b, e)) : add2(h, pair_of<T>(b, e));
+            else if (gain) h = mul2(h, pair_of<T>(g, e));
+            set_pair(o, e, h);
         }
-        st_vec<T, N>(y + c, o);
+        st_vec<T, W>(y + v * W, o);
     }
 }
 
-// rows too wide for a block's registers: three passes, the second and third from the L2 cache
+// rows too wide for the kernels above: three walks, the second and third from the caches
 template <class T, bool LAYER>
 __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a)
 {
+    constexpr int W = 16 / sizeof(T);
     __shared__ float buf[2][32];
-    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(blockIdx.x) * a.d;
-    T *y = static_cast<T *>(a.y) + static_cast<size_t>(blockIdx.x) * a.d;
+    const size_t first = static_cast<size_t>(blockIdx.x) * a.d;
+    Place<T> at{a.d, static_cast<int>(first % W), 0};
+    at.nv = (at.shift + a.d + W - 1) / W;
+    const T *x = static_cast<const T *>(a.x) + first - at.shift;
+    T *y = static_cast<T *>(a.y) + first - at.shift;
     const T *gain = static_cast<const T *>(a.gain), *bias = static_cast<const T *>(a.bias);
-    float mean = 0.f, s = 0.f;
+    const float inv = 1.f / static_cast<float>(a.d);
+    float mean = 0.f;
     if constexpr (LAYER) {
-        for (int c = threadIdx.x; c < a.d; c += blockDim.x) s += to_f32(x[c]);
-        mean = row_sum<false>(s, buf[0]) / static_cast<float>(a.d);
+        F2 s = f2(0.f, 0.f);
+        for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
+            const uint4 u = at.load(x, v);
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) s = add2(s, pair_of<T>(u, e));
+        }
+        mean = row_sum<false>(both(s), buf[0]) * inv;
     }
-    float q = 0.f;
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        const float z = to_f32(x[c]) - mean;
-        q = fmaf(z, z, q);
+    F2 q = f2(0.f, 0.f);
+    for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
+        const uint4 u = at.load(x, v);
+        const bool in = at.inner(v);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) {
+            F2 c = pair_of<T>(u, e);
+            if constexpr (LAYER) c = add2(c, f2(in || at.has(v, 2 * e) ? -mean : 0.f, in || at.has(v, 2 * e + 1) ? -mean : 0.f));
+            q = fma2(c, c, q);
+        }
     }
-    const float r = 1.f / sqrtf(row_sum<false>(q, buf[1]) / static_cast<float>(a.d) + a.eps);
-    if (threadIdx.x == 0 && a.stats) {
-        a.stats[2 * static_cast<size_t>(blockIdx.x)] = mean;
-        a.stats[2 * static_cast<size_t>(blockIdx.x) + 1] = r;
+    const float r = 1.f / sqrtf(row_sum<false>(both(q), buf[1]) * inv + a.eps);
+    if (threadIdx.x == 0 && a.stats)
+        *reinterpret_cast<float2 *>(a.stats + 2 * static_cast<size_t>(blockIdx.x)) = make_float2(mean, r);
+    for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
+        const Vec<T, W> u = as_vec<T>(at.load(x, v));
+        const int c0 = v * W - at.shift;
+        Vec<T, W> o;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int c = min(max(c0 + e, 0), a.d - 1);
+            float h = (to_f32(u.v[e]) - mean) * r;
+            if (gain) h *= to_f32(__ldg(gain + c));
+            if (LAYER && bias) h += to_f32(__ldg(bias + c));
+            o.v[e] = from_f32<T>(h);
+        }
+        at.store(y, v, o);
     }
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        float h = (to_f32(x[c]) - mean) * r;
-        if (gain) h *= to_f32(gain[c]);
-        if (LAYER && bias) h += to_f32(bias[c]);
-        y[c] = from_f32<T>(h);
+}
+
+// ---- rows through a ring of shared memory ---------------------------------------------------
+
+__device__ __forceinline__ void row_copy16(uint32_t dst, const void *src, int bytes)
+{
+    // bytes (1 .. 16) are read, the rest of the 16 is filled with 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void row_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void row_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 row_lds(uint32_t p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+constexpr int kRowStages = 3, kGradStages = 2;   // rows of a ring, forward and backward
+constexpr int kGradThreads = 384;                // two blocks an SM leave each thread 85 registers
+
+// The rows of one block (or warp): row, row + step, ... of one class, n of them.
+template <class T, bool WARP>
+struct Rows {
+    static constexpr int W = 16 / sizeof(T);
+    Place<T> at;
+    int nt, tid;                // threads of a row
+    int row, step, n;
+    __device__ __forceinline__ Rows(int T_, int d, int P)
+    {
+        nt = WARP ? 32 : blockDim.x;
+        tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+        const int cls = blockIdx.x % P, per = WARP ? kRowWarps : 1;
+        at.d = d;
+        at.shift = static_cast<int>(static_cast<long>(cls) * d % W);
+        at.nv = (at.shift + d + W - 1) / W;
+        row = cls + P * static_cast<int>((blockIdx.x / P) * per + (WARP ? threadIdx.x >> 5 : 0));
+        step = static_cast<int>(gridDim.x / P) * per * P;
+        n = row < T_ ? (T_ - 1 - row) / step + 1 : 0;
+    }
+    // this thread's first vector of the first row
+    template <class V> __device__ __forceinline__ V *start(V *p) const
+    {
+        return p + (static_cast<long>(row) * at.d - at.shift + tid * W);
+    }
+    // one value per column (gain, bias) at the columns' places, fill where there is none
+    __device__ __forceinline__ void columns(char *dst, const void *src, float fill) const
+    {
+        T *out = reinterpret_cast<T *>(dst);
+        for (int i = threadIdx.x; i < at.nv * W; i += blockDim.x) {
+            const int c = i - at.shift;
+            out[i] = src && c >= 0 && c < at.d ? static_cast<const T *>(src)[c] : from_f32<T>(fill);
+        }
+    }
+};
+
+// the forward pass for rows that are no multiple of 16 bytes
+template <class T, int NV, bool LAYER, bool WARP>
+__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 512) norm_shift_kernel(NormArgs a, int P)
+{
+    constexpr int W = 16 / sizeof(T);
+    extern __shared__ __align__(16) char row_smem[];
+    __shared__ float buf[4][32];
+    const Rows<T, WARP> rows(a.T, a.d, P);
+    const Place<T> &at = rows.at;
+    const int nt = rows.nt, tid = rows.tid, plane = nt * NV * 16;
+    rows.columns(row_smem, a.gain, 1.f);
+    if (LAYER) rows.columns(row_smem + plane, a.bias, 0.f);
+    const uint32_t gains = smem_u32(row_smem) + tid * 16, biases = gains + plane;
+    const uint32_t ring = gains + (LAYER ? 2 : 1) * plane + (WARP ? (threadIdx.x >> 5) * (kRowStages * plane) : 0);
+    __syncthreads();
+    const T *src = rows.start(static_cast<const T *>(a.x));
+    T *dst = rows.start(static_cast<T *>(a.y));
+    const long stride = static_cast<long>(rows.step) * a.d;
+    int bytes[NV];              // 0: no such vector
+    bool whole[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * nt + tid;
+        bytes[i] = v < at.nv ? at.bytes(v) : 0;
+        whole[i] = at.inner(v);
+    }
+    int left = rows.n, put = 0;
+    auto issue = [&]() {
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (bytes[i]) row_copy16(ring + put * plane + i * nt * 16, src + i * nt * W, bytes[i]);
+        }
+        row_commit();
+        --left;
+        src += stride;
+        put = put + 1 == kRowStages ? 0 : put + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kRowStages - 1; ++i) issue();
+    const float inv = 1.f / static_cast<float>(a.d);
+    float2 *stats = reinterpret_cast<float2 *>(a.stats) + rows.row;
+    int get = 0, parity = 0;
+    for (int j = 0; j < rows.n; ++j) {
+        issue();
+        row_wait<kRowStages - 1>();
+        const uint32_t st = ring + get * plane;
+        get = get + 1 == kRowStages ? 0 : get + 1;
+        uint4 u[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            u[i] = bytes[i] ? row_lds(st + i * nt * 16) : make_uint4(0, 0, 0, 0);
+            if (bytes[i] && !whole[i]) u[i] = bits_and(u[i], at.keep(i * nt + tid));
+        }
+        float mean = 0.f;
+        if constexpr (LAYER) {
+            F2 s = f2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) s = add2(s, pair_of<T>(u[i], e));
+            mean = row_sum<WARP>(both(s), buf[parity]) * inv;
+        }
+        const F2 nm = f2(-mean, -mean);
+        F2 q = f2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!bytes[i]) continue;
+            const int v = i * nt + tid;
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) {
+                F2 c = pair_of<T>(u[i], e);
+                if constexpr (LAYER)
+                    c = add2(c, whole[i] ? nm : f2(at.has(v, 2 * e) ? -mean : 0.f, at.has(v, 2 * e + 1) ? -mean : 0.f));
+                q = fma2(c, c, q);
+            }
+        }
+        const float r = 1.f / sqrtf(row_sum<WARP>(both(q), buf[2 + parity]) * inv + a.eps);
+        parity ^= 1;
+        if (tid == 0 && a.stats) *stats = make_float2(mean, r);
+        stats += rows.step;
+        const F2 rr = f2(r, r);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!bytes[i]) continue;
+            const uint4 g = row_lds(gains + i * nt * 16);
+            uint4 b;
+            if constexpr (LAYER) b = row_lds(biases + i * nt * 16);
+            Vec<T, W> o;
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) {
+                const F2 x = pair_of<T>(u[i], e);
+                if constexpr (LAYER) set_pair(o, e, fma2(mul2(add2(x, nm), rr), pair_of<T>(g, e), pair_of<T>(b, e)));
+                else set_pair(o, e, mul2(mul2(x, rr), pair_of<T>(g, e)));
+            }
+            T *p = dst + i * nt * W;
+            if (whole[i]) {
+                st_vec<T, W>(p, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (at.has(i * nt + tid, e)) p[e] = o.v[e];
+            }
+        }
+        dst += stride;
     }
 }
 
 // ---- backward ------------------------------------------------------------------------
 
-// the two row means of the gradient at once: one barrier a row (buffers by turns)
+// the two row sums of the gradient at once: one barrier a row (buffers by turns)
 template <bool LAYER, bool WARP>
 __device__ __forceinline__ float2 row_sums(float s0, float s1, float2 *buf)
 {
@@ -147,136 +410,281 @@ __device__ __forceinline__ float2 row_sums(float s0, float s1, float2 *buf)
     return make_float2(LAYER ? warp_sum(w.x) : 0.f, warp_sum(w.y));
 }
 
-template <class T, int N, int NV, bool LAYER, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 512) norm_grad_kernel(NormArgs a)
+__device__ __forceinline__ float half_of(F2 a, int e) { return e & 1 ? unpack(a).y : unpack(a).x; }
+
+// With h = dy g:  dx = r h - r mean(h) - xh (r mean(h xh)).  SHIFT: rows that are no multiple of 16 bytes.
+// The arithmetic (about 18 instructions an element, half of them conversions) runs close to the
+// memory traffic, so what a thread needs again after the row's sums it keeps as fp32 pairs where the
+// registers allow it.
+template <class T, int NV, bool LAYER, bool WARP, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : NV > 2 ? 512 : kGradThreads, WARP ? 5 : NV > 2 ? 1 : 2)
+    norm_grad_kernel(NormArgs a, int P)
 {
+    constexpr int W = 16 / sizeof(T);
+    constexpr bool kHold = NV * W <= 8 || (NV * W <= 16 && !LAYER);
+    extern __shared__ __align__(16) char row_smem[];
     __shared__ float2 buf[2][32];
     griddep_launch_dependents();   // the reduction's blocks wait for this kernel's end by themselves
-    const int nt = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int rows = WARP ? kRowWarps : 1;
-    const T *gain = static_cast<const T *>(a.gain);
+    const Rows<T, WARP> rows(a.T, a.d, P);
+    const Place<T> &at = rows.at;
+    const int nt = rows.nt, tid = rows.tid, plane = nt * NV * 16;
+    // the gain: shifted rows take it from shared memory, others through the L1 cache, which leaves the rings more room
+    const uint32_t gains = smem_u32(row_smem) + tid * 16;
+    const uint4 *gain16 = static_cast<const uint4 *>(a.gain) + tid;
+    if (SHIFT) {
+        rows.columns(row_smem, a.gain, 1.f);
+        __syncthreads();
+    }
+    auto gain_of = [&](int i) {
+        if (SHIFT) return row_lds(gains + i * nt * 16);
+        if (a.gain) return __ldg(gain16 + i * nt);
+        Vec<T, W> one;
+#pragma unroll
+        for (int e = 0; e < W; ++e) one.v[e] = from_f32<T>(1.f);
+        uint4 u;
+        memcpy(&u, one.v, 16);
+        return u;
+    };
+    const uint32_t ring = gains + (SHIFT ? plane : 0) + (WARP ? (threadIdx.x >> 5) * (kGradStages * 2 * plane) : 0);
+    const T *xs = rows.start(static_cast<const T *>(a.x)), *ds = rows.start(static_cast<const T *>(a.dy));
+    T *dst = rows.start(static_cast<T *>(a.dx));
+    const long stride = static_cast<long>(rows.step) * a.d;
+    int bytes[NV];              // 0: no such vector
+    bool whole[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * nt + tid;
+        bytes[i] = v < at.nv ? (SHIFT ? at.bytes(v) : 16) : 0;
+        whole[i] = !SHIFT || at.inner(v);
+    }
+    const float2 *stats = reinterpret_cast<const float2 *>(a.stats) + rows.row;
+    int left = rows.n, put = 0;
+    // the next row's copies, and its statistics
+    auto issue = [&]() {
+        float2 st = make_float2(0.f, 0.f);
+        if (left > 0) {
+            st = __ldg(stats);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!bytes[i]) continue;
+                const uint32_t to = ring + put * (2 * plane) + i * nt * 16;
+                row_copy16(to, xs + i * nt * W, SHIFT ? bytes[i] : 16);
+                row_copy16(to + plane, ds + i * nt * W, SHIFT ? bytes[i] : 16);
+            }
+        }
+        row_commit();
+        --left;
+        stats += rows.step;
+        xs += stride;
+        ds += stride;
+        put = put + 1 == kGradStages ? 0 : put + 1;
+        return st;
+    };
+    static_assert(kGradStages == 2, "one row's statistics are on their way");
+    float2 coming = issue();
     const float inv = 1.f / static_cast<float>(a.d);
-    float dg[NV][N], db[LAYER ? NV : 1][LAYER ? N : 1];
+    F2 dg[NV][W / 2], db[LAYER ? NV : 1][W / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            dg[i][e] = 0.f;
-            if constexpr (LAYER) db[i][e] = 0.f;
+        for (int e = 0; e < W / 2; ++e) {
+            dg[i][e] = f2(0.f, 0.f);
+            if constexpr (LAYER) db[i][e] = f2(0.f, 0.f);
         }
-    int parity = 0;
-    for (int row = blockIdx.x * rows + (WARP ? threadIdx.x >> 5 : 0); row < a.T; row += gridDim.x * rows) {
-        const size_t at = static_cast<size_t>(row) * a.d;
-        const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
-        T *dx = static_cast<T *>(a.dx) + at;
-        Vec<T, N> xv[NV], dv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((i * nt + tid) * N < a.d) {
-                xv[i] = ld_vec<T, N>(x + (i * nt + tid) * N);
-                dv[i] = ld_vec<T, N>(dy + (i * nt + tid) * N);
-            }
-        const float2 st = __ldg(reinterpret_cast<const float2 *>(a.stats) + row);
-        const float mean = LAYER ? st.x : 0.f, r = st.y;
-        float s0 = 0.f, s1 = 0.f;
+    int get = 0, parity = 0;
+    for (int j = 0; j < rows.n; ++j) {
+        const float2 now = coming;
+        coming = issue();
+        row_wait<kGradStages - 1>();
+        const uint32_t st = ring + get * (2 * plane);
+        get = get + 1 == kGradStages ? 0 : get + 1;
+        // kept from the sums to the results: xh and h, or the row as it came
+        F2 xh[NV][W / 2], h[NV][W / 2];
+        uint4 xr[NV], dr[NV];
+        const F2 nm = f2(-now.x, -now.x), rr = f2(now.y, now.y);
+        F2 t0 = f2(0.f, 0.f), t1 = f2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + tid) * N;
-            if (c >= a.d) continue;
-            Vec<T, N> g;
-            if (gain) g = ld_vec<T, N>(gain + c);
+            if (!bytes[i]) continue;
+            uint4 xu = row_lds(st + i * nt * 16), du = row_lds(st + plane + i * nt * 16);
+            if (!whole[i]) {   // values of the neighbouring rows: 0
+                const uint4 k = at.keep(i * nt + tid);
+                xu = bits_and(xu, k);
+                du = bits_and(du, k);
+            }
+            const uint4 gu = gain_of(i);
+            if constexpr (!kHold) {
+                xr[i] = xu;
+                dr[i] = du;
+            }
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float dyv = to_f32(dv[i].v[e]), xh = (to_f32(xv[i].v[e]) - mean) * r;
-                const float h = gain ? dyv * to_f32(g.v[e]) : dyv;
-                s1 = fmaf(h, xh, s1);
-                dg[i][e] = fmaf(dyv, xh, dg[i][e]);
+            for (int e = 0; e < W / 2; ++e) {
+                const F2 dy = pair_of<T>(du, e), hv = mul2(dy, pair_of<T>(gu, e));
+                F2 c = pair_of<T>(xu, e);
                 if constexpr (LAYER) {
-                    s0 += h;
-                    db[i][e] += dyv;
+                    c = add2(c, nm);
+                    t0 = add2(t0, hv);
+                    db[i][e] = add2(db[i][e], dy);
+                }
+                const F2 xv = mul2(c, rr);
+                t1 = fma2(hv, xv, t1);
+                dg[i][e] = fma2(dy, xv, dg[i][e]);
+                if constexpr (kHold) {
+                    h[i][e] = hv;
+                    xh[i][e] = xv;
                 }
             }
         }
-        const float2 s = row_sums<LAYER, WARP>(s0, s1, buf[parity]);
+        const float2 s = row_sums<LAYER, WARP>(both(t0), both(t1), buf[parity]);
         parity ^= 1;
-        const float m0 = s.x * inv, m1 = s.y * inv;
+        const float m0 = -now.y * (s.x * inv), m1 = -now.y * (s.y * inv);
+        const F2 k0 = f2(m0, m0), k1 = f2(m1, m1);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + tid) * N;
-            if (c >= a.d) continue;
-            Vec<T, N> g, o;
-            if (gain) g = ld_vec<T, N>(gain + c);
+            if (!bytes[i]) continue;
+            uint4 gu;
+            if constexpr (!kHold) gu = gain_of(i);
+            Vec<T, W> o;
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float xh = (to_f32(xv[i].v[e]) - mean) * r;
-                float h = to_f32(dv[i].v[e]);
-                if (gain) h *= to_f32(g.v[e]);
-                o.v[e] = from_f32<T>(r * (fmaf(-xh, m1, h) - m0));
+            for (int e = 0; e < W / 2; ++e) {
+                F2 xv, hv;
+                if constexpr (kHold) {
+                    xv = xh[i][e];
+                    hv = h[i][e];
+                } else {
+                    hv = mul2(pair_of<T>(dr[i], e), pair_of<T>(gu, e));
+                    xv = pair_of<T>(xr[i], e);
+                    if constexpr (LAYER) xv = add2(xv, nm);
+                    xv = mul2(xv, rr);
+                }
+                set_pair(o, e, fma2(xv, k1, LAYER ? fma2(hv, rr, k0) : mul2(hv, rr)));
             }
-            st_vec<T, N>(dx + c, o);
+            T *p = dst + i * nt * W;
+            if (whole[i]) {
+                st_vec<T, W>(p, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (at.has(i * nt + tid, e)) p[e] = o.v[e];
+            }
         }
+        dst += stride;
     }
     // the block's sums, one row of [2, d]; a warp per row: the warps' sums joined in order first
     float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
     if constexpr (WARP) {
-        __shared__ float sum[LAYER ? 2 : 1][32 * NV * N];
+        row_wait<0>();
+        __syncthreads();
+        float *sum = reinterpret_cast<float *>(row_smem);   // the rows' space is free now
+        constexpr int kSum = 32 * NV * W;
         for (int w = 0; w < kRowWarps; ++w) {
             if (static_cast<int>(threadIdx.x >> 5) == w) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const int c = (i * 32 + tid) * N + e;
-                        sum[0][c] = w ? sum[0][c] + dg[i][e] : dg[i][e];
-                        if constexpr (LAYER) sum[1][c] = w ? sum[1][c] + db[i][e] : db[i][e];
+                    for (int e = 0; e < W; ++e) {
+                        const int c = (i * 32 + tid) * W + e;
+                        sum[c] = w ? sum[c] + half_of(dg[i][e / 2], e) : half_of(dg[i][e / 2], e);
+                        if constexpr (LAYER)
+                            sum[kSum + c] = w ? sum[kSum + c] + half_of(db[i][e / 2], e) : half_of(db[i][e / 2], e);
                     }
             }
             __syncthreads();
         }
         for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-            part[c] = sum[0][c];
-            if constexpr (LAYER) part[a.d + c] = sum[1][c];
+            part[c] = sum[c + at.shift];
+            if constexpr (LAYER) part[a.d + c] = sum[kSum + c + at.shift];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + tid) * N;
-            if (c >= a.d) continue;
+            const int v = i * nt + tid;
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                part[c + e] = dg[i][e];
-                if constexpr (LAYER) part[a.d + c + e] = db[i][e];
-            }
+            for (int e = 0; e < W; ++e)
+                if (at.has(v, e)) {
+                    part[v * W + e - at.shift] = half_of(dg[i][e / 2], e);
+                    if constexpr (LAYER) part[a.d + v * W + e - at.shift] = half_of(db[i][e / 2], e);
+                }
         }
     }
 }
 
-// dx of rows too wide for the registers
-template <class T, bool LAYER>
-__global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormArgs a)
+// Rows wider than that: the second walk reads them from the caches, and the columns' sums (SUMS) are in
+// shared memory, each column its thread's own.
+template <class T, bool LAYER, bool SUMS>
+__global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormArgs a, int P)
 {
-    __shared__ float2 buf[32];
-    const size_t at = static_cast<size_t>(blockIdx.x) * a.d;
-    const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
+    constexpr int W = 16 / sizeof(T);
+    extern __shared__ __align__(16) char row_smem[];
+    __shared__ float2 buf[2][32];
+    griddep_launch_dependents();
+    const Rows<T, false> rows(a.T, a.d, P);
+    const Place<T> &at = rows.at;
+    float *dg = reinterpret_cast<float *>(row_smem), *db = dg + at.nv * W;
+    if (SUMS)
+        for (int i = threadIdx.x; i < at.nv * W * (LAYER ? 2 : 1); i += blockDim.x) dg[i] = 0.f;
+    __syncthreads();
     const T *gain = static_cast<const T *>(a.gain);
-    T *dx = static_cast<T *>(a.dx) + at;
-    const float mean = LAYER ? a.stats[2 * static_cast<size_t>(blockIdx.x)] : 0.f;
-    const float r = a.stats[2 * static_cast<size_t>(blockIdx.x) + 1];
-    float s0 = 0.f, s1 = 0.f;
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        const float h = gain ? to_f32(dy[c]) * to_f32(gain[c]) : to_f32(dy[c]);
-        s0 += h;
-        s1 = fmaf(h, (to_f32(x[c]) - mean) * r, s1);
+    const bool gains16 = gain && at.shift == 0;
+    auto gain_of = [&](int v) {
+        if (gains16 && at.inner(v)) return as_vec<T>(__ldg(reinterpret_cast<const uint4 *>(gain + v * W)));
+        Vec<T, W> g;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int c = min(max(v * W + e - at.shift, 0), a.d - 1);
+            g.v[e] = gain ? __ldg(gain + c) : from_f32<T>(1.f);
+        }
+        return g;
+    };
+    const float inv = 1.f / static_cast<float>(a.d);
+    int parity = 0;
+    for (int j = 0; j < rows.n; ++j) {
+        const int row = rows.row + j * rows.step;
+        const long first = static_cast<long>(row) * a.d - at.shift;
+        const T *x = static_cast<const T *>(a.x) + first, *dy = static_cast<const T *>(a.dy) + first;
+        T *dx = static_cast<T *>(a.dx) + first;
+        const float mean = LAYER ? a.stats[2 * static_cast<size_t>(row)] : 0.f, r = a.stats[2 * static_cast<size_t>(row) + 1];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll 2
+        for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
+            const Vec<T, W> xv = as_vec<T>(at.load(x, v)), dv = as_vec<T>(at.load(dy, v)), g = gain_of(v);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                // outside the row both are 0: dy is 0 in every term
+                const float c = to_f32(xv.v[e]) - mean, h = to_f32(dv.v[e]) * to_f32(g.v[e]);
+                s0 += h;
+                s1 = fmaf(h, c, s1);
+                if (SUMS) {
+                    dg[v * W + e] = fmaf(to_f32(dv.v[e]), c * r, dg[v * W + e]);
+                    if (LAYER) db[v * W + e] += to_f32(dv.v[e]);
+                }
+            }
+        }
+        const float2 s = row_sums<LAYER, false>(s0, s1, buf[parity]);
+        parity ^= 1;
+        const float m0 = -r * (s.x * inv), m1 = -(r * (s.y * inv)) * r;
+#pragma unroll 2
+        for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
+            const Vec<T, W> xv = as_vec<T>(at.load(x, v)), dv = as_vec<T>(at.load(dy, v)), g = gain_of(v);
+            Vec<T, W> o;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float c = to_f32(xv.v[e]) - mean, h = to_f32(dv.v[e]) * to_f32(g.v[e]);
+                o.v[e] = from_f32<T>(fmaf(c * r, m1, fmaf(h, r, m0)));
+            }
+            at.store(dx, v, o);
+        }
     }
-    const float2 s = row_sums<LAYER, false>(s0, s1, buf);
-    const float inv = 1.f / static_cast<float>(a.d), m0 = s.x * inv, m1 = s.y * inv;
+    if (!SUMS) return;
+    __syncthreads();
+    float *part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
     for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-        const float h = gain ? to_f32(dy[c]) * to_f32(gain[c]) : to_f32(dy[c]);
-        dx[c] = from_f32<T>(r * (fmaf(-(to_f32(x[c]) - mean) * r, m1, h) - m0));
+        part[c] = dg[c + at.shift];
+        if (LAYER) part[a.d + c] = db[c + at.shift];
     }
 }
 
-// partial column sums of those rows: a block takes 32 columns of every gridDim.y-th group of 8 rows
+// partial column sums of rows whose sums do not fit shared memory: a block takes 32 columns of every gridDim.y-th group of 8 rows
 template <class T, bool LAYER>
 __global__ void __launch_bounds__(256) norm_grad_columns_kernel(NormArgs a)
 {
@@ -302,10 +710,10 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(NormArgs a)
     a.part[(static_cast<size_t>(blockIdx.y) * 2 + threadIdx.y) * a.d + c] = s;
 }
 
-// dgain / dbias = the sum of the blocks' partial rows, in block order within each of 8 strands
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *part, int parts, int d, float *dgain, float *dbias)
+// dgain / dbias = the sum of the blocks' partial rows, in block order within each of 32 strands
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *part, int parts, int d, float *dgain, float *dbias)
 {
-    __shared__ float red[8][32];
+    __shared__ float red[32][33];
     griddep_wait();
     float *out = blockIdx.y ? dbias : dgain;
     const int c = blockIdx.x * 32 + threadIdx.x;
@@ -313,97 +721,171 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *part, int
     float s = 0.f;
     if (c < d) {
         const float *p = part + static_cast<size_t>(blockIdx.y) * d + c;
-#pragma unroll 8
-        for (int i = threadIdx.y; i < parts; i += 8) s += __ldcg(p + static_cast<size_t>(i) * 2 * d);
+        for (int i0 = threadIdx.y; i0 < parts; i0 += 32 * 8) {
+            float v[8];   // in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i0 + 32 * k < parts ? __ldcg(p + static_cast<size_t>(i0 + 32 * k) * 2 * d) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
     }
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y || c >= d) return;
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) t += red[w][threadIdx.x];
-    out[c] = t;
+    // warp y joins the strands of column y
+    const float t = warp_sum(red[threadIdx.x][threadIdx.y]);
+    const int col = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && col < d) out[col] = t;
 }
 
 // ---- host -------------------------------------------------------------------------------
 
-// most rows of partial sums a backward call keeps: the blocks of the widest launch
-int most_parts(int d) { return d <= 4096 ? 4 * kSms : d <= 16384 ? 2 * kSms : 64; }
+// most rows of partial sums a backward call keeps, the blocks of its launch: a multiple of 8, the most classes of
+// rows.  Narrow rows leave room for 8 blocks an SM, as long as each has some ten rows to walk over.
+int most_parts(int T, int d)
+{
+    if (d > 4096) return d <= 8192 ? 2 * kSms : d <= 32768 ? 152 : 64;
+    const int walk = T / 80 * 8;
+    return walk > 8 * kSms ? 8 * kSms : walk < 2 * kSms ? 2 * kSms : walk;
+}
 
 int parts_for(int T, int d)
 {
-    const int most = most_parts(d);
-    return T < most ? T : most;
+    const int most = most_parts(T, d), rows = (T + 7) / 8 * 8;
+    return rows < most ? rows : most;
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-template <class T, int N, bool LAYER>
+// classes of rows that begin at the same place within 16 bytes
+int classes_of(int d, int W)
+{
+    int P = 1;
+    while (static_cast<long>(P) * d % W) P *= 2;
+    return P;
+}
+
+constexpr int kRowSmem = 225 * 1024;   // shared memory a ring may take
+
+// A launch of one of the ring kernels: planes of shared memory for the columns and for the ring of a row, and
+// blocks that fill the SMs by shared memory and registers, a multiple of P.
+struct RingPlan {
+    int block, grid;
+    size_t smem;
+    bool ok;
+};
+
+RingPlan ring_plan(int T, int nv, int NV, bool warp, int P, int columns, int planes, int most, int regs)
+{
+    RingPlan r;
+    r.block = warp ? kRowWarps * 32 : round32((nv + NV - 1) / NV);
+    const int nt = warp ? 32 : r.block;
+    const size_t plane = static_cast<size_t>(nt) * NV * 16;
+    r.smem = plane * columns + plane * planes * (warp ? kRowWarps : 1);
+    r.ok = r.block <= 512 && r.smem <= static_cast<size_t>(kRowSmem);
+    int occ = static_cast<int>(220 * 1024 / (r.smem + 1024));
+    const int by_regs = 65536 / (regs * r.block);
+    occ = occ < by_regs ? occ : by_regs;
+    const int per = warp ? kRowWarps : 1, work = (T + per - 1) / per;
+    int grid = kSms * (occ > 1 ? occ : 1);
+    grid = grid < work ? grid : work;
+    grid = grid < most ? grid : most;
+    r.grid = (grid + P - 1) / P * P;
+    return r;
+}
+
+inline cudaError_t launch_ring(void (*kernel)(NormArgs, int), const RingPlan &r, const NormArgs &a, int P, cudaStream_t s)
+{
+    if (r.smem > 40 * 1024) {   // near the 48 KB that need no leave, static arrays included
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(r.smem));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+    }
+    return op_launch(kernel, dim3(r.grid), dim3(r.block), r.smem, s, false, 1, a, P);
+}
+
+template <class T, bool LAYER>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t s)
 {
-    constexpr int NW = N > 2 ? 4 : 8;                 // vectors a thread, by their size
-    const int nvec = a.d / N;
-    if (nvec <= 32 * NW)
-        return op_launch(norm_kernel<T, N, NW, LAYER, true>, dim3((a.T + kRowWarps - 1) / kRowWarps), dim3(kRowWarps * 32), 0,
-                         s, false, 1, a);
-    if (nvec <= 1024 * NW)
-        return op_launch(norm_kernel<T, N, NW, LAYER, false>, dim3(a.T), dim3(round32((nvec + NW - 1) / NW)), 0, s, false, 1,
-                         a);
-    if constexpr (N > 2) {
+    constexpr int W = 16 / sizeof(T);
+    const int P = classes_of(a.d, W);
+    if (P == 1) {
+        const int nvec = a.d / W;
+        if (nvec <= 32 * 4)
+            return op_launch(norm_kernel<T, 4, LAYER, true>, dim3((a.T + kRowWarps - 1) / kRowWarps), dim3(kRowWarps * 32), 0,
+                             s, false, 1, a);
+        if (nvec <= 1024 * 4)
+            return op_launch(norm_kernel<T, 4, LAYER, false>, dim3(a.T), dim3(round32((nvec + 3) / 4)), 0, s, false, 1, a);
         if (nvec <= 1024 * 8)
-            return op_launch(norm_kernel<T, N, 8, LAYER, false>, dim3(a.T), dim3(round32((nvec + 7) / 8)), 0, s, false, 1, a);
+            return op_launch(norm_kernel<T, 8, LAYER, false>, dim3(a.T), dim3(round32((nvec + 7) / 8)), 0, s, false, 1, a);
+    } else {
+        const int nv = (a.d + 2 * (W - 1)) / W;   // at the largest shift
+        const bool warp = nv <= 32 * 2;
+        const RingPlan r = ring_plan(a.T, nv, 2, warp, P, LAYER ? 2 : 1, kRowStages, 1 << 20, 64);
+        if (r.ok)
+            return launch_ring(warp ? norm_shift_kernel<T, 2, LAYER, true> : norm_shift_kernel<T, 2, LAYER, false>, r, a, P, s);
     }
     return op_launch(norm_wide_kernel<T, LAYER>, dim3(a.T), dim3(1024), 0, s, false, 1, a);
 }
 
-template <class T, int N, bool LAYER>
-cudaError_t launch_norm_grad(const NormArgs &a, cudaStream_t s)
+template <class T, bool LAYER, bool SHIFT>
+cudaError_t launch_norm_grad_ring(const RingPlan &r, bool warp, int NV, const NormArgs &a, int P, cudaStream_t s)
 {
-    constexpr int NW = N > 2 ? 4 : 8;
-    const int nvec = a.d / N;
-    int parts = parts_for(a.T, a.d);
-    cudaError_t e;
-    if (nvec <= 32 * NW) {
-        const int blocks = (a.T + kRowWarps - 1) / kRowWarps;
-        parts = blocks < parts ? blocks : parts;
-        e = op_launch(norm_grad_kernel<T, N, NW, LAYER, true>, dim3(parts), dim3(kRowWarps * 32), 0, s, false, 1, a);
-    } else if (nvec <= 512 * NW) {
-        e = op_launch(norm_grad_kernel<T, N, NW, LAYER, false>, dim3(parts), dim3(round32((nvec + NW - 1) / NW)), 0, s, false,
-                      1, a);
-    } else {
-        e = op_launch(norm_grad_wide_kernel<T, LAYER>, dim3(a.T), dim3(1024), 0, s, false, 1, a);
-        if (e != cudaSuccess || (!a.dgain && !a.dbias)) return e;
-        const int groups = (a.T + 7) / 8;
-        parts = groups < parts ? groups : parts;
-        parts = parts < 64 ? parts : 64;
-        e = op_launch(norm_grad_columns_kernel<T, LAYER>, dim3((a.d + 31) / 32, parts), dim3(32, 8), 0, s, false, 1, a);
-    }
-    if (e != cudaSuccess || (!a.dgain && !a.dbias)) return e;
-    return op_launch(norm_reduce_kernel, dim3((a.d + 31) / 32, a.dbias ? 2 : 1), dim3(32, 8), 0, s, true, 1,
-                     static_cast<const float *>(a.part), parts, a.d, a.dgain, a.dbias);
+    return launch_ring(warp     ? norm_grad_kernel<T, 2, LAYER, true, SHIFT>
+                       : NV > 2 ? norm_grad_kernel<T, 4, LAYER, false, SHIFT>
+                                : norm_grad_kernel<T, 2, LAYER, false, SHIFT>,
+                       r, a, P, s);
 }
 
-template <class T, int N>
-cudaError_t norm_by_kind(int kind, bool grad, const NormArgs &a, cudaStream_t s)
+template <class T, bool LAYER>
+cudaError_t launch_norm_grad(const NormArgs &a, cudaStream_t s)
 {
-    if (kind == MOE_NORM_LAYER) return grad ? launch_norm_grad<T, N, true>(a, s) : launch_norm<T, N, true>(a, s);
-    return grad ? launch_norm_grad<T, N, false>(a, s) : launch_norm<T, N, false>(a, s);
+    constexpr int W = 16 / sizeof(T);
+    const int P = classes_of(a.d, W), nv = (a.d + (P > 1 ? 2 : 1) * (W - 1)) / W;
+    const bool warp = nv <= 32 * 2, sums = a.dgain || a.dbias;
+    const int NV = nv <= 2 * kGradThreads ? 2 : 4;
+    RingPlan r = ring_plan(a.T, nv, NV, warp, P, P > 1, 2 * kGradStages, most_parts(a.T, a.d), warp ? 96 : NV > 2 ? 128 : 80);
+    cudaError_t e;
+    if (r.ok) {
+        e = P == 1 ? launch_norm_grad_ring<T, LAYER, false>(r, warp, NV, a, P, s)
+                   : launch_norm_grad_ring<T, LAYER, true>(r, warp, NV, a, P, s);
+    } else {
+        // one block an SM: the sums take its shared memory
+        r.block = 1024;
+        r.smem = static_cast<size_t>(nv) * W * 4 * (LAYER ? 2 : 1);
+        const bool fits = sums && r.smem <= static_cast<size_t>(kRowSmem);
+        const int most = parts_for(a.T, a.d);
+        r.grid = a.T < kSms ? a.T : kSms;
+        if (fits && r.grid > most) r.grid = most;
+        r.grid = (r.grid + P - 1) / P * P;
+        if (!fits) r.smem = 0;
+        e = launch_ring(fits ? norm_grad_wide_kernel<T, LAYER, true> : norm_grad_wide_kernel<T, LAYER, false>, r, a, P, s);
+        if (e == cudaSuccess && sums && !fits) {
+            const int groups = (a.T + 7) / 8;
+            r.grid = groups < most ? groups : most;
+            r.grid = r.grid < 64 ? r.grid : 64;
+            e = op_launch(norm_grad_columns_kernel<T, LAYER>, dim3((a.d + 31) / 32, r.grid), dim3(32, 8), 0, s, false, 1, a);
+        }
+    }
+    if (e != cudaSuccess || !sums) return e;
+    return op_launch(norm_reduce_kernel, dim3((a.d + 31) / 32, a.dbias ? 2 : 1), dim3(32, 32), 0, s, true, 1,
+                     static_cast<const float *>(a.part), r.grid, a.d, a.dgain, a.dbias);
 }
 
 template <class T>
-cudaError_t norm_by_width(int kind, bool grad, const NormArgs &a, cudaStream_t s)
+cudaError_t norm_by_kind(int kind, bool grad, const NormArgs &a, cudaStream_t s)
 {
-    constexpr int W = 16 / sizeof(T);
-    if (a.d % W == 0) return norm_by_kind<T, W>(kind, grad, a, s);
-    if (a.d % 2 == 0) return norm_by_kind<T, 2>(kind, grad, a, s);
-    return norm_by_kind<T, 1>(kind, grad, a, s);
+    if (kind == MOE_NORM_LAYER) return grad ? launch_norm_grad<T, true>(a, s) : launch_norm<T, true>(a, s);
+    return grad ? launch_norm_grad<T, false>(a, s) : launch_norm<T, false>(a, s);
 }
 
 int norm_dispatch(int kind, int dtype, bool grad, const NormArgs &a, cudaStream_t s)
 {
-    const cudaError_t e = dtype == MOE_F32   ? norm_by_width<float>(kind, grad, a, s)
-                          : dtype == MOE_F16 ? norm_by_width<__half>(kind, grad, a, s)
-                                             : norm_by_width<__nv_bfloat16>(kind, grad, a, s);
+    const cudaError_t e = dtype == MOE_F32   ? norm_by_kind<float>(kind, grad, a, s)
+                          : dtype == MOE_F16 ? norm_by_kind<__half>(kind, grad, a, s)
+                                             : norm_by_kind<__nv_bfloat16>(kind, grad, a, s);
     return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
 

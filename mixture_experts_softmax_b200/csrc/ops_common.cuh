@@ -7,6 +7,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstring>
+#include <type_traits>
+
 #include "../../include/moe.h"
 #include "ptx.cuh"
 
@@ -80,22 +83,27 @@ struct alignas((N * sizeof(T) >= 16) ? 16 : N * sizeof(T)) Vec {
     T v[N];
 };
 
-// read once, not read again by this kernel: do not keep it in L1
+// through the read-only path: what is loaded must not be written by the same kernel
 template <class T, int N>
 __device__ __forceinline__ Vec<T, N> ld_vec(const T *p)
 {
     Vec<T, N> r;
     constexpr int B = N * sizeof(T);
     if constexpr (B >= 16) {
-        uint4 *w = reinterpret_cast<uint4 *>(r.v);
 #pragma unroll
-        for (int i = 0; i < B / 16; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < B / 16; ++i) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            memcpy(reinterpret_cast<char *>(r.v) + 16 * i, &w, 16);
+        }
     } else if constexpr (B == 8) {
-        *reinterpret_cast<uint2 *>(r.v) = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+        memcpy(r.v, &w, 8);
     } else if constexpr (B == 4) {
-        *reinterpret_cast<uint32_t *>(r.v) = __ldg(reinterpret_cast<const uint32_t *>(p));
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
+        memcpy(r.v, &w, 4);
     } else {
-        *reinterpret_cast<uint16_t *>(r.v) = __ldg(reinterpret_cast<const uint16_t *>(p));
+        const uint16_t w = __ldg(reinterpret_cast<const uint16_t *>(p));
+        memcpy(r.v, &w, 2);
     }
     return r;
 }
@@ -105,15 +113,94 @@ __device__ __forceinline__ void st_vec(T *p, const Vec<T, N> &r)
 {
     constexpr int B = N * sizeof(T);
     if constexpr (B >= 16) {
-        const uint4 *w = reinterpret_cast<const uint4 *>(r.v);
 #pragma unroll
-        for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
+        for (int i = 0; i < B / 16; ++i) {
+            uint4 w;
+            memcpy(&w, reinterpret_cast<const char *>(r.v) + 16 * i, 16);
+            reinterpret_cast<uint4 *>(p)[i] = w;
+        }
     } else if constexpr (B == 8) {
-        *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(r.v);
+        uint2 w;
+        memcpy(&w, r.v, 8);
+        *reinterpret_cast<uint2 *>(p) = w;
     } else if constexpr (B == 4) {
-        *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(r.v);
+        uint32_t w;
+        memcpy(&w, r.v, 4);
+        *reinterpret_cast<uint32_t *>(p) = w;
     } else {
-        *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(r.v);
+        p[0] = r.v[0];
+    }
+}
+
+// two fp32 values in one 64-bit register pair: sm_100 adds, multiplies and fuses both in one instruction
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// elements 2 i and 2 i + 1 of 16 bytes of T as fp32, and the way back
+template <class T> __device__ __forceinline__ F2 pair_of(const uint4 &u, int i);
+__device__ __forceinline__ uint32_t word_of(const uint4 &u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
+template <> __device__ __forceinline__ F2 pair_of<float>(const uint4 &u, int i)
+{
+    return f2(__uint_as_float(word_of(u, 2 * i)), __uint_as_float(word_of(u, 2 * i + 1)));
+}
+template <> __device__ __forceinline__ F2 pair_of<__nv_bfloat16>(const uint4 &u, int i)
+{
+    const uint32_t w = word_of(u, i);
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ F2 pair_of<__half>(const uint4 &u, int i)
+{
+    const uint32_t w = word_of(u, i);
+    __half2 h;
+    memcpy(&h, &w, 4);
+    const float2 f = __half22float2(h);
+    return f2(f.x, f.y);
+}
+template <class T, int N> __device__ __forceinline__ void set_pair(Vec<T, N> &o, int i, F2 a)
+{
+    const float2 f = unpack(a);
+    if constexpr (sizeof(T) == 4) {
+        o.v[2 * i] = f.x;
+        o.v[2 * i + 1] = f.y;
+    } else if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        o.v[2 * i] = h.x;
+        o.v[2 * i + 1] = h.y;
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        o.v[2 * i] = h.x;
+        o.v[2 * i + 1] = h.y;
     }
 }
 

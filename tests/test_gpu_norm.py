@@ -75,16 +75,19 @@ def test_norm(m, T, d, dt, kind):
         ops64.assert_close(got[2], want[2], tols[2], "dbias")
 
 
-@pytest.mark.parametrize("T,d", [(3000, 96), (2500, 8200), (4000, 19), (1300, 6144), (1000, 16400)])
+@pytest.mark.parametrize("T,d", [(3000, 96), (2500, 8200), (4000, 19), (1300, 6144), (1000, 16400), (3001, 1537),
+                                 (1999, 4100), (901, 12001), (2111, 1022), (640, 16384)])
 @pytest.mark.parametrize("kind", [0, 1])
-def test_norm_many_rows(m, T, d, kind):
-    """More rows than blocks: every block sums over several."""
-    x, gain, bias, dy = inputs(T, d, 0, kind == 1)
-    y, stats = run_forward(m, kind, 0, x, gain, bias)
-    ref, _, tol, _ = ops64.norm(x, gain, bias, float(torch.tensor(1e-5)), kind == 1, DT[0])
+@pytest.mark.parametrize("dt", [0, 2])
+def test_norm_many_rows(m, T, d, kind, dt):
+    """More rows than blocks: every block sums over several, of each of the classes of rows that begin at the same
+    place within 16 bytes."""
+    x, gain, bias, dy = inputs(T, d, dt, kind == 1)
+    y, stats = run_forward(m, kind, dt, x, gain, bias)
+    ref, _, tol, _ = ops64.norm(x, gain, bias, float(torch.tensor(1e-5)), kind == 1, DT[dt])
     ops64.assert_close(y, ref, tol, "y")
-    got = run_backward(m, kind, 0, x, gain, stats, dy, kind == 1)
-    want, tols = ops64.norm_grad(x, gain, stats, dy, kind == 1, DT[0])
+    got = run_backward(m, kind, dt, x, gain, stats, dy, kind == 1)
+    want, tols = ops64.norm_grad(x, gain, stats, dy, kind == 1, DT[dt])
     for a, b, t in list(zip(got, want, tols))[:2 + kind]:
         ops64.assert_close(a, b, t)
 
