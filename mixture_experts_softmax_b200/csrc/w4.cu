@@ -6,7 +6,7 @@
 // With few rows the weights' bytes bound it: each is read once, by asynchronous 16-byte copies into
 // a ring of stages that every lane keeps for itself, so that the copies of the next stages run while one is
 // multiplied.  The products run on mma.sync m16n8k16 with 16 features as rows and 8 token rows as
-// columns: a weight enters as the exact 16-bit float of its value, the fp32 sum over one group is
+// columns: a weight enters as an exact 16-bit float, the fp32 sum over one group is
 // multiplied by the group's scale and added up in fp32.  (The tcgen05 path wants both operands
 // staged as 16-bit tiles; for 8 columns that staging alone moves four times the weights' bytes through shared memory.)
 //
@@ -134,16 +134,52 @@ __device__ __forceinline__ uint4 lds128(uint32_t p)
     return v;
 }
 
-// Two 4-bit values of w (bits 4 i .. and 16 + 4 i ..) as exact 16-bit floats: OR-ed into the mantissa of
-// 128 (bf16) or 1024 (fp16), whose last place is 1, then 128 + 8 (1024 + 8) subtracted.
+// (w & mask) | bits in one instruction: both constants come from registers
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
+{
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(bits));
+    return v;
+}
+template <class T2>
+__device__ __forceinline__ uint32_t bits_of(const T2 &v)
+{
+    uint32_t w;
+    memcpy(&w, &v, 4);
+    return w;
+}
+template <class T2>
+__device__ __forceinline__ T2 as16(uint32_t w)
+{
+    T2 v;
+    memcpy(&v, &w, 4);
+    return v;
+}
+
+// The four operand pairs of a word of 4-bit values: five integer operations and four 16-bit FMAs for
+// eight weights (the integer pipe is the one that limits this kernel, so the FMAs do what they can).
+//
+// bf16: an integer v below 256 in the low byte of a half is the bf16 v * 2^-133, on both sides of
+// the smallest normal number.  A mask leaves u or 16 u there (u = value + 8), and an exact FMA makes
+// (u - 8) / 128 of it; the joined sums are taken 128 times.
+// fp16: the same bits OR-ed into 1024, whose last place is 1, are 1024 + u and 1024 + 16 u; an exact
+// FMA makes u - 8.
 template <class T> struct Deq;
 template <> struct Deq<__nv_bfloat16> {
-    template <int I>
-    static __device__ __forceinline__ uint32_t pair(uint32_t w)
+    static constexpr float kScale = 128.f;
+    __nv_bfloat162 lo, hi, off;
+    uint32_t m0, m1;
+    __device__ __forceinline__ Deq()
+        : lo(__floats2bfloat162_rn(0x1p126f, 0x1p126f)), hi(__floats2bfloat162_rn(0x1p122f, 0x1p122f)),
+          off(__floats2bfloat162_rn(-0.0625f, -0.0625f)), m0(0x000f000fu), m1(0x00f000f0u)
     {
-        uint32_t v = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&v), __floats2bfloat162_rn(136.f, 136.f));
-        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) const
+    {
+        const uint32_t h = w >> 8;
+        const uint32_t v[4] = {w & m0, w & m1, h & m0, h & m1};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = bits_of(__hfma2(as16<__nv_bfloat162>(v[i]), i & 1 ? hi : lo, off));
     }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
@@ -154,12 +190,20 @@ template <> struct Deq<__nv_bfloat16> {
     }
 };
 template <> struct Deq<__half> {
-    template <int I>
-    static __device__ __forceinline__ uint32_t pair(uint32_t w)
+    static constexpr float kScale = 1.f;
+    __half2 lo, hi, off, offhi;
+    uint32_t m0, m1, one;
+    __device__ __forceinline__ Deq()
+        : lo(__floats2half2_rn(1.f, 1.f)), hi(__floats2half2_rn(0.0625f, 0.0625f)), off(__floats2half2_rn(-1032.f, -1032.f)),
+          offhi(__floats2half2_rn(-72.f, -72.f)), m0(0x000f000fu), m1(0x00f000f0u), one(0x64006400u)
     {
-        uint32_t v = ((w >> (4 * I)) & 0x000f000fu) | 0x64006400u;
-        const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&v), __floats2half2_rn(1032.f, 1032.f));
-        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) const
+    {
+        const uint32_t h = w >> 8;
+        const uint32_t v[4] = {and_or(w, m0, one), and_or(w, m1, one), and_or(h, m0, one), and_or(h, m1, one)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = bits_of(__hfma2(as16<__half2>(v[i]), i & 1 ? hi : lo, i & 1 ? offhi : off));
     }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
@@ -229,6 +273,7 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
     const uint32_t xaddr = smem_u32(xs) + g * kXStride + c * 32;
 
+    const Deq<T> deq;
     float acc[2][NB][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -306,8 +351,8 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t v = half ? (j ? w[t].w : w[t].z) : (j ? w[t].y : w[t].x);
-                            const uint32_t av[4] = {Deq<T>::template pair<0>(v), Deq<T>::template pair<1>(v),
-                                                    Deq<T>::template pair<2>(v), Deq<T>::template pair<3>(v)};
+                            uint32_t av[4];
+                            deq.operands(v, av);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
                                 Deq<T>::mma(part[t][nb], av, j ? xv[nb].z : xv[nb].x, j ? xv[nb].w : xv[nb].y);
@@ -355,6 +400,8 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
                 for (int q = 0; q < (GATED ? 2 : 1); ++q)
                     v[q] += src[(kp * fw + q * fwt + f / kBlockF) * kWarpRed + n * kRedStride + f % kBlockF];
         }
+        v[0] *= Deq<T>::kScale;
+        v[1] *= Deq<T>::kScale;
         const float y = GATED ? gelu_of(v[0]) * v[1] : v[0];
         const size_t at = static_cast<size_t>(row0 + n) * a.N + feature;
         if (a.out_f32) static_cast<float *>(a.y)[at] = y;
