@@ -50,11 +50,9 @@ __device__ __forceinline__ float row_sum(float v, float *buf)
 }
 
 template <class T>
-__device__ __forceinline__ Vec<T, 16 / sizeof(T)> as_vec(uint4 u)
+__device__ __forceinline__ void st_words(T *p, const uint32_t (&w)[4])
 {
-    Vec<T, 16 / sizeof(T)> r;
-    memcpy(r.v, &u, 16);
-    return r;
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // where the vectors of a row are: column c of a row is element c + shift of the vectors that hold it
@@ -84,21 +82,26 @@ struct Place {
     __device__ __forceinline__ uint4 load(const T *p, int v) const
     {
         if (inner(v)) return __ldg(reinterpret_cast<const uint4 *>(p + v * W));
-        Vec<T, W> r;
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < W; ++e) r.v[e] = has(v, e) ? p[v * W + e] : from_f32<T>(0.f);
-        uint4 u;
-        memcpy(&u, r.v, 16);
-        return u;
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (W == 4) {
+                w[j] = has(v, j) ? __float_as_uint(p[v * W + j]) : 0u;
+            } else {
+                const uint16_t *h = reinterpret_cast<const uint16_t *>(p + v * W) + 2 * j;
+                w[j] = (has(v, 2 * j) ? h[0] : 0u) | (has(v, 2 * j + 1) ? static_cast<uint32_t>(h[1]) << 16 : 0u);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ void store(T *p, int v, const Vec<T, W> &o) const
+    // the elements of vector v, at p, that are this row's
+    __device__ __forceinline__ void store_part(T *p, int v, const uint32_t (&w)[4]) const
     {
-        if (inner(v)) {
-            st_vec<T, W>(p + v * W, o);
-        } else {
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (has(v, e)) p[v * W + e] = o.v[e];
+        for (int e = 0; e < W; ++e) {
+            if (!has(v, e)) continue;
+            if constexpr (W == 4) p[e] = __uint_as_float(w[e]);
+            else reinterpret_cast<uint16_t *>(p)[e] = static_cast<uint16_t>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
         }
     }
 };
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) norm_kernel(Norm
         uint4 g, b;
         if (gain) g = __ldg(gain + v);
         if (LAYER && bias) b = __ldg(bias + v);
-        Vec<T, W> o;
+        uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < W / 2; ++e) {
             F2 h = pair_of<T>(u[i], e);
@@ -170,9 +173,9 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) norm_kernel(Norm
             h = mul2(h, rr);
             if (LAYER && bias) h = gain ? fma2(h, pair_of<T>(g, e), pair_of<T>(b, e)) : add2(h, pair_of<T>(b, e));
             else if (gain) h = mul2(h, pair_of<T>(g, e));
-            set_pair(o, e, h);
+            set_pair<T>(o, e, h);
         }
-        st_vec<T, W>(y + v * W, o);
+        st_words(y + v * W, o);
     }
 }
 
@@ -214,18 +217,19 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a)
     if (threadIdx.x == 0 && a.stats)
         *reinterpret_cast<float2 *>(a.stats + 2 * static_cast<size_t>(blockIdx.x)) = make_float2(mean, r);
     for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
-        const Vec<T, W> u = as_vec<T>(at.load(x, v));
+        const uint4 u = at.load(x, v);
         const int c0 = v * W - at.shift;
-        Vec<T, W> o;
+        uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const int c = min(max(c0 + e, 0), a.d - 1);
-            float h = (to_f32(u.v[e]) - mean) * r;
-            if (gain) h *= to_f32(__ldg(gain + c));
-            if (LAYER && bias) h += to_f32(__ldg(bias + c));
-            o.v[e] = from_f32<T>(h);
+        for (int e = 0; e < W / 2; ++e) {
+            const int c = min(max(c0 + 2 * e, 0), a.d - 1), c1 = min(max(c0 + 2 * e + 1, 0), a.d - 1);
+            F2 h = mul2(add2(pair_of<T>(u, e), f2(-mean, -mean)), f2(r, r));
+            if (gain) h = mul2(h, f2(to_f32(__ldg(gain + c)), to_f32(__ldg(gain + c1))));
+            if (LAYER && bias) h = add2(h, f2(to_f32(__ldg(bias + c)), to_f32(__ldg(bias + c1))));
+            set_pair<T>(o, e, h);
         }
-        at.store(y, v, o);
+        if (at.inner(v)) st_words(y + v * W, o);
+        else at.store_part(y + v * W, v, o);
     }
 }
 
@@ -374,21 +378,16 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 512) norm_shift_kernel
             const uint4 g = row_lds(gains + i * nt * 16);
             uint4 b;
             if constexpr (LAYER) b = row_lds(biases + i * nt * 16);
-            Vec<T, W> o;
+            uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) {
                 const F2 x = pair_of<T>(u[i], e);
-                if constexpr (LAYER) set_pair(o, e, fma2(mul2(add2(x, nm), rr), pair_of<T>(g, e), pair_of<T>(b, e)));
-                else set_pair(o, e, mul2(mul2(x, rr), pair_of<T>(g, e)));
+                if constexpr (LAYER) set_pair<T>(o, e, fma2(mul2(add2(x, nm), rr), pair_of<T>(g, e), pair_of<T>(b, e)));
+                else set_pair<T>(o, e, mul2(mul2(x, rr), pair_of<T>(g, e)));
             }
             T *p = dst + i * nt * W;
-            if (whole[i]) {
-                st_vec<T, W>(p, o);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    if (at.has(i * nt + tid, e)) p[e] = o.v[e];
-            }
+            if (whole[i]) st_words(p, o);
+            else at.store_part(p, i * nt + tid, o);
         }
         dst += stride;
     }
@@ -438,12 +437,8 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : NV > 2 ? 512 : kGradTh
     auto gain_of = [&](int i) {
         if (SHIFT) return row_lds(gains + i * nt * 16);
         if (a.gain) return __ldg(gain16 + i * nt);
-        Vec<T, W> one;
-#pragma unroll
-        for (int e = 0; e < W; ++e) one.v[e] = from_f32<T>(1.f);
-        uint4 u;
-        memcpy(&u, one.v, 16);
-        return u;
+        const uint32_t one = W == 4 ? __float_as_uint(1.f) : pack2<T>(1.f, 1.f);
+        return make_uint4(one, one, one, one);
     };
     const uint32_t ring = gains + (SHIFT ? plane : 0) + (WARP ? (threadIdx.x >> 5) * (kGradStages * 2 * plane) : 0);
     const T *xs = rows.start(static_cast<const T *>(a.x)), *ds = rows.start(static_cast<const T *>(a.dy));
@@ -544,7 +539,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : NV > 2 ? 512 : kGradTh
             if (!bytes[i]) continue;
             uint4 gu;
             if constexpr (!kHold) gu = gain_of(i);
-            Vec<T, W> o;
+            uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) {
                 F2 xv, hv;
@@ -557,16 +552,11 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : NV > 2 ? 512 : kGradTh
                     if constexpr (LAYER) xv = add2(xv, nm);
                     xv = mul2(xv, rr);
                 }
-                set_pair(o, e, fma2(xv, k1, LAYER ? fma2(hv, rr, k0) : mul2(hv, rr)));
+                set_pair<T>(o, e, fma2(xv, k1, LAYER ? fma2(hv, rr, k0) : mul2(hv, rr)));
             }
             T *p = dst + i * nt * W;
-            if (whole[i]) {
-                st_vec<T, W>(p, o);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    if (at.has(i * nt + tid, e)) p[e] = o.v[e];
-            }
+            if (whole[i]) st_words(p, o);
+            else at.store_part(p, i * nt + tid, o);
         }
         dst += stride;
     }
@@ -626,15 +616,11 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormArgs a, int P)
     __syncthreads();
     const T *gain = static_cast<const T *>(a.gain);
     const bool gains16 = gain && at.shift == 0;
-    auto gain_of = [&](int v) {
-        if (gains16 && at.inner(v)) return as_vec<T>(__ldg(reinterpret_cast<const uint4 *>(gain + v * W)));
-        Vec<T, W> g;
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const int c = min(max(v * W + e - at.shift, 0), a.d - 1);
-            g.v[e] = gain ? __ldg(gain + c) : from_f32<T>(1.f);
-        }
-        return g;
+    auto gain_of = [&](int v, uint4 u, int e) {   // pair e of vector v's gains (u: loaded whole)
+        if (gains16 && at.inner(v)) return pair_of<T>(u, e);
+        const int c = v * W + 2 * e - at.shift;
+        return gain ? f2(to_f32(__ldg(gain + min(max(c, 0), a.d - 1))), to_f32(__ldg(gain + min(max(c + 1, 0), a.d - 1))))
+                    : f2(1.f, 1.f);
     };
     const float inv = 1.f / static_cast<float>(a.d);
     int parity = 0;
@@ -644,35 +630,48 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormArgs a, int P)
         const T *x = static_cast<const T *>(a.x) + first, *dy = static_cast<const T *>(a.dy) + first;
         T *dx = static_cast<T *>(a.dx) + first;
         const float mean = LAYER ? a.stats[2 * static_cast<size_t>(row)] : 0.f, r = a.stats[2 * static_cast<size_t>(row) + 1];
-        float s0 = 0.f, s1 = 0.f;
+        const F2 nm = f2(-mean, -mean), rr = f2(r, r);
+        F2 t0 = f2(0.f, 0.f), t1 = f2(0.f, 0.f);
 #pragma unroll 2
         for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
-            const Vec<T, W> xv = as_vec<T>(at.load(x, v)), dv = as_vec<T>(at.load(dy, v)), g = gain_of(v);
+            const uint4 xu = at.load(x, v), du = at.load(dy, v);
+            const uint4 gu = gains16 && at.inner(v) ? __ldg(reinterpret_cast<const uint4 *>(gain + v * W)) : make_uint4(0, 0, 0, 0);
+            F2 *sg = reinterpret_cast<F2 *>(dg + v * W), *sb = reinterpret_cast<F2 *>(db + v * W);
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
+            for (int e = 0; e < W / 2; ++e) {
                 // outside the row both are 0: dy is 0 in every term
-                const float c = to_f32(xv.v[e]) - mean, h = to_f32(dv.v[e]) * to_f32(g.v[e]);
-                s0 += h;
-                s1 = fmaf(h, c, s1);
-                if (SUMS) {
-                    dg[v * W + e] = fmaf(to_f32(dv.v[e]), c * r, dg[v * W + e]);
-                    if (LAYER) db[v * W + e] += to_f32(dv.v[e]);
+                const F2 dv = pair_of<T>(du, e), h = mul2(dv, gain_of(v, gu, e));
+                F2 c = pair_of<T>(xu, e);
+                if constexpr (LAYER) {
+                    c = add2(c, nm);
+                    t0 = add2(t0, h);
+                }
+                const F2 xh = mul2(c, rr);
+                t1 = fma2(h, xh, t1);
+                if constexpr (SUMS) {
+                    sg[e] = fma2(dv, xh, sg[e]);
+                    if constexpr (LAYER) sb[e] = add2(sb[e], dv);
                 }
             }
         }
-        const float2 s = row_sums<LAYER, false>(s0, s1, buf[parity]);
+        const float2 s = row_sums<LAYER, false>(both(t0), both(t1), buf[parity]);
         parity ^= 1;
-        const float m0 = -r * (s.x * inv), m1 = -(r * (s.y * inv)) * r;
+        const float m0 = -r * (s.x * inv), m1 = -r * (s.y * inv);
+        const F2 k0 = f2(m0, m0), k1 = f2(m1, m1);
 #pragma unroll 2
         for (int v = threadIdx.x; v < at.nv; v += blockDim.x) {
-            const Vec<T, W> xv = as_vec<T>(at.load(x, v)), dv = as_vec<T>(at.load(dy, v)), g = gain_of(v);
-            Vec<T, W> o;
+            const uint4 xu = at.load(x, v), du = at.load(dy, v);
+            const uint4 gu = gains16 && at.inner(v) ? __ldg(reinterpret_cast<const uint4 *>(gain + v * W)) : make_uint4(0, 0, 0, 0);
+            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const float c = to_f32(xv.v[e]) - mean, h = to_f32(dv.v[e]) * to_f32(g.v[e]);
-                o.v[e] = from_f32<T>(fmaf(c * r, m1, fmaf(h, r, m0)));
+            for (int e = 0; e < W / 2; ++e) {
+                const F2 h = mul2(pair_of<T>(du, e), gain_of(v, gu, e));
+                F2 c = pair_of<T>(xu, e);
+                if constexpr (LAYER) c = add2(c, nm);
+                set_pair<T>(o, e, fma2(mul2(c, rr), k1, LAYER ? fma2(h, rr, k0) : mul2(h, rr)));
             }
-            at.store(dx, v, o);
+            if (at.inner(v)) st_words(dx + v * W, o);
+            else at.store_part(dx + v * W, v, o);
         }
     }
     if (!SUMS) return;

@@ -77,60 +77,85 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N consecutive elements, held as they are in memory; moved in 16-byte pieces where N spans them
+// two fp32 values as one word of a 16-bit type
+template <class T> __device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    uint32_t w;
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        memcpy(&w, &h, 4);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        memcpy(&w, &h, 4);
+    }
+    return w;
+}
+
+// N consecutive elements as the words they are in memory (16-bit elements unpacked one by one would take
+// a register each)
 template <class T, int N>
-struct alignas((N * sizeof(T) >= 16) ? 16 : N * sizeof(T)) Vec {
-    T v[N];
+struct Raw {
+    static constexpr int B = N * static_cast<int>(sizeof(T)), NW = (B + 3) / 4;
+    uint32_t w[NW];
+    // through the read-only path: what is loaded must not be written by the same kernel
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (B >= 16) {
+#pragma unroll
+            for (int i = 0; i < NW / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = u.x;
+                w[4 * i + 1] = u.y;
+                w[4 * i + 2] = u.z;
+                w[4 * i + 3] = u.w;
+            }
+        } else if constexpr (B == 8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = u.x;
+            w[1] = u.y;
+        } else if constexpr (B == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        } else {
+            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+        if constexpr (B >= 16) {
+#pragma unroll
+            for (int i = 0; i < NW / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (B == 8) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (B == 4) {
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+        } else {
+            *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
+        }
+    }
+    // element e (a constant after unrolling)
+    __device__ __forceinline__ float get(int e) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[e]);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            __half2 h;
+            memcpy(&h, &w[e / 2], 4);
+            return e & 1 ? __high2float(h) : __low2float(h);
+        } else {
+            return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        }
+    }
+    // all elements, from f(e)
+    template <class F> __device__ __forceinline__ void set(F &&f)
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f(i));
+            else w[i] = pack2<T>(f(2 * i), N > 1 ? f(2 * i + 1) : 0.f);
+        }
+    }
 };
-
-// through the read-only path: what is loaded must not be written by the same kernel
-template <class T, int N>
-__device__ __forceinline__ Vec<T, N> ld_vec(const T *p)
-{
-    Vec<T, N> r;
-    constexpr int B = N * sizeof(T);
-    if constexpr (B >= 16) {
-#pragma unroll
-        for (int i = 0; i < B / 16; ++i) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-            memcpy(reinterpret_cast<char *>(r.v) + 16 * i, &w, 16);
-        }
-    } else if constexpr (B == 8) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-        memcpy(r.v, &w, 8);
-    } else if constexpr (B == 4) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
-        memcpy(r.v, &w, 4);
-    } else {
-        const uint16_t w = __ldg(reinterpret_cast<const uint16_t *>(p));
-        memcpy(r.v, &w, 2);
-    }
-    return r;
-}
-
-template <class T, int N>
-__device__ __forceinline__ void st_vec(T *p, const Vec<T, N> &r)
-{
-    constexpr int B = N * sizeof(T);
-    if constexpr (B >= 16) {
-#pragma unroll
-        for (int i = 0; i < B / 16; ++i) {
-            uint4 w;
-            memcpy(&w, reinterpret_cast<const char *>(r.v) + 16 * i, 16);
-            reinterpret_cast<uint4 *>(p)[i] = w;
-        }
-    } else if constexpr (B == 8) {
-        uint2 w;
-        memcpy(&w, r.v, 8);
-        *reinterpret_cast<uint2 *>(p) = w;
-    } else if constexpr (B == 4) {
-        uint32_t w;
-        memcpy(&w, r.v, 4);
-        *reinterpret_cast<uint32_t *>(p) = w;
-    } else {
-        p[0] = r.v[0];
-    }
-}
 
 // two fp32 values in one 64-bit register pair: sm_100 adds, multiplies and fuses both in one instruction
 struct F2 {
@@ -187,20 +212,15 @@ template <> __device__ __forceinline__ F2 pair_of<__half>(const uint4 &u, int i)
     const float2 f = __half22float2(h);
     return f2(f.x, f.y);
 }
-template <class T, int N> __device__ __forceinline__ void set_pair(Vec<T, N> &o, int i, F2 a)
+// pair i of 16 bytes of T
+template <class T> __device__ __forceinline__ void set_pair(uint32_t (&w)[4], int i, F2 a)
 {
     const float2 f = unpack(a);
     if constexpr (sizeof(T) == 4) {
-        o.v[2 * i] = f.x;
-        o.v[2 * i + 1] = f.y;
-    } else if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __floats2half2_rn(f.x, f.y);
-        o.v[2 * i] = h.x;
-        o.v[2 * i + 1] = h.y;
+        w[2 * i] = __float_as_uint(f.x);
+        w[2 * i + 1] = __float_as_uint(f.y);
     } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-        o.v[2 * i] = h.x;
-        o.v[2 * i + 1] = h.y;
+        w[i] = pack2<T>(f.x, f.y);
     }
 }
 

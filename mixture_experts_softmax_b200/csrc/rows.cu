@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(256) unsort_kernel(UnsortArgs a, int vpr, long
         // the loads of a group of picks are in flight together
         int row[kGroup];
         float g[kGroup];
-        Vec<R, N> v[kGroup];
+        Raw<R, N> v[kGroup];
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) {
             row[j] = j0 + j < a.k ? __ldg(a.slot + t * a.k + j0 + j) : -1;
@@ -319,25 +319,25 @@ __global__ void __launch_bounds__(256) unsort_kernel(UnsortArgs a, int vpr, long
         }
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
-            if (row[j] >= 0 && row[j] < n) v[j] = ld_vec<R, N>(rows + static_cast<size_t>(row[j]) * a.d);
+            if (row[j] >= 0 && row[j] < n) v[j].load(rows + static_cast<size_t>(row[j]) * a.d);
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
             if (row[j] >= 0 && row[j] < n) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] = fmaf(g[j], to_f32(v[j].v[e]), acc[e]);
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(g[j], v[j].get(e), acc[e]);
             }
     }
-    Vec<O, N> o;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o.v[e] = from_f32<O>(acc[e]);
-    st_vec<O, N>(static_cast<O *>(a.out) + static_cast<size_t>(t) * a.d + c, o);
+    Raw<O, N> o;
+    o.set([&](int e) { return acc[e]; });
+    o.store(static_cast<O *>(a.out) + static_cast<size_t>(t) * a.d + c);
 }
 
 // ---- the gradient of the way back -----------------------------------------------------
 //
-// NT threads take a token: they read dout[t] once per group of four picks (from the L1 cache after
-// the first), write each pick's gradient row and add up the products for its gate's gradient in
-// fp32, joined over the threads in a fixed tree.
+// NT threads take a token.  For a group of G picks a thread has kSteps vectors of dout[t] and of every
+// pick's row in flight together (more picks read dout[t] again, from the caches); it writes the
+// picks' gradient rows and adds up the products for the gates' gradients in fp32, joined over
+// the threads in a fixed tree.
 
 struct UnsortGradArgs {
     int T, k, d;
@@ -348,65 +348,80 @@ struct UnsortGradArgs {
     float *dgate;               // nullptr: not wanted
 };
 
-template <class R, class O, int N, int NT>
+template <class R, class O, int N, int G, int NT>
 __global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a)
 {
     constexpr int kTokens = 256 / NT, kWarps = NT / 32;
-    __shared__ float red[2][kTokens * kWarps][kGroup];
+    // vectors of a row in flight: about 192 bytes a thread
+    constexpr int kBytes = N * static_cast<int>(sizeof(O) + G * sizeof(R));
+    constexpr int kSteps = kBytes >= 96 ? 2 : kBytes >= 48 ? 3 : kBytes >= 20 ? 4 : 8;
+    __shared__ float red[2][kTokens * kWarps][G];
     const int n = a.T * a.k, lane = threadIdx.x % NT, sub = threadIdx.x / NT;
     const int t = blockIdx.x * kTokens + sub;
     if (NT == 32 && t >= a.T) return;   // NT == 256: the grid is T blocks
     const O *dout = static_cast<const O *>(a.dout) + static_cast<size_t>(t) * a.d;
     int parity = 0;
-    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-        int row[kGroup];
-        float g[kGroup], dot[kGroup];
+    for (int j0 = 0; j0 < a.k; j0 += G) {
+        bool on[G];
+        const R *src[G];
+        R *dst[G];
+        float g[G], dot[G];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            const bool on = j0 + j < a.k;
-            row[j] = on ? __ldg(a.slot + t * a.k + j0 + j) : -1;
-            if (row[j] >= n) row[j] = -1;
-            g[j] = on && a.gate ? __ldg(a.gate + t * a.k + j0 + j) : 1.f;
+        for (int j = 0; j < G; ++j) {
+            const int row = j0 + j < a.k ? __ldg(a.slot + t * a.k + j0 + j) : -1;
+            on[j] = row >= 0 && row < n;
+            const size_t at = on[j] ? static_cast<size_t>(row) * a.d : 0;
+            src[j] = static_cast<const R *>(a.rows) + at;
+            dst[j] = static_cast<R *>(a.drows) + at;
+            g[j] = on[j] && a.gate ? __ldg(a.gate + t * a.k + j0 + j) : 1.f;
             dot[j] = 0.f;
         }
-#pragma unroll 2
-        for (int c = lane * N; c < a.d; c += NT * N) {
-            const Vec<O, N> dv = ld_vec<O, N>(dout + c);
-            Vec<R, N> rv[kGroup];
-            if (a.dgate) {
+        for (int c0 = lane * N; c0 < a.d; c0 += NT * N * kSteps) {
+            Raw<O, N> dv[kSteps];
+            Raw<R, N> rv[kSteps][G];
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    if (row[j] >= 0)
-                        rv[j] = ld_vec<R, N>(static_cast<const R *>(a.rows) + static_cast<size_t>(row[j]) * a.d + c);
-            }
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                if (row[j] < 0) continue;
-                Vec<R, N> o;
-#pragma unroll
-                for (int e = 0; e < N; ++e) o.v[e] = from_f32<R>(g[j] * to_f32(dv.v[e]));
-                st_vec<R, N>(static_cast<R *>(a.drows) + static_cast<size_t>(row[j]) * a.d + c, o);
+            for (int u = 0; u < kSteps; ++u) {
+                const int c = c0 + u * NT * N;
+                if (c >= a.d) continue;
+                dv[u].load(dout + c);
                 if (a.dgate) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) dot[j] = fmaf(to_f32(dv.v[e]), to_f32(rv[j].v[e]), dot[j]);
+                    for (int j = 0; j < G; ++j)
+                        if (on[j]) rv[u][j].load(src[j] + c);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int c = c0 + u * NT * N;
+                if (c >= a.d) continue;
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    if (!on[j]) continue;
+                    Raw<R, N> o;
+                    o.set([&](int e) { return g[j] * dv[u].get(e); });
+                    o.store(dst[j] + c);
+                    if (a.dgate) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) dot[j] = fmaf(dv[u].get(e), rv[u][j].get(e), dot[j]);
+                    }
                 }
             }
         }
         if (!a.dgate) continue;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) dot[j] = warp_sum(dot[j]);
+        for (int j = 0; j < G; ++j) dot[j] = warp_sum(dot[j]);
         if constexpr (NT == 32) {
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j)
+            for (int j = 0; j < G; ++j)
                 if (lane == j && j0 + j < a.k) a.dgate[t * a.k + j0 + j] = dot[j];
         } else {
             // two buffers by turns: one barrier a group
             if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j) red[parity][threadIdx.x >> 5][j] = dot[j];
+                for (int j = 0; j < G; ++j) red[parity][threadIdx.x >> 5][j] = dot[j];
             }
             __syncthreads();
-            if (lane < kGroup && j0 + lane < a.k) {
+            if (lane < G && j0 + lane < a.k) {
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) s += red[parity][w][lane];
@@ -429,9 +444,12 @@ cudaError_t launch_unsort(const UnsortArgs &a, cudaStream_t s)
 template <class R, class O, int N>
 cudaError_t launch_unsort_grad(const UnsortGradArgs &a, cudaStream_t s)
 {
-    if (a.d / N <= 128)   // a warp covers the row in four steps
-        return op_launch(unsort_grad_kernel<R, O, N, 32>, dim3((a.T + 7) / 8), dim3(256), 0, s, false, 1, a);
-    return op_launch(unsort_grad_kernel<R, O, N, 256>, dim3(a.T), dim3(256), 0, s, false, 1, a);
+    const dim3 grid(a.d / N <= 128 ? (a.T + 7) / 8 : a.T);   // a warp covers 128 vectors in a few steps
+    if (a.k <= 2)
+        return op_launch(a.d / N <= 128 ? unsort_grad_kernel<R, O, N, 2, 32> : unsort_grad_kernel<R, O, N, 2, 256>, grid,
+                         dim3(256), 0, s, false, 1, a);
+    return op_launch(a.d / N <= 128 ? unsort_grad_kernel<R, O, N, 4, 32> : unsort_grad_kernel<R, O, N, 4, 256>, grid,
+                     dim3(256), 0, s, false, 1, a);
 }
 
 // the vector width by the row width: 16 bytes of the wider type's neighbour where d allows
