@@ -23,10 +23,11 @@ constexpr int kMaxPicks = 16;
 
 // ---- the order -------------------------------------------------------------------
 //
-// The routes are cut into one contiguous segment per warp.  Every warp counts its segment's routes
-// per expert, a scan over warps (and blocks) turns the counts into each warp's first row of every
-// expert, and a second walk over the segment places its routes: lanes with the same expert find
-// one another with a match, so a route's rank is the number of earlier lanes of its group.
+// The routes are cut into one contiguous segment per warp.  A warp walks over its segment, counts the
+// routes per expert and notes each one's rank among those: lanes with the same expert find one
+// another by votes, so the rank is the count so far plus the number of earlier lanes of the group.
+// A scan over warps (and blocks) turns the counts into each warp's first row of every expert, and
+// a second, cheap walk adds that to the ranks.
 
 struct SortArgs {
     int T, k, E, n;             // n = T * k
@@ -42,77 +43,120 @@ __device__ __forceinline__ int expert_of(const SortArgs &a, int r)
     return e >= 0 && e < a.E ? e : -1;
 }
 
-// counts of the segment [begin, end) into cnt[E] (this warp's own)
-__device__ __forceinline__ void count_segment(const SortArgs &a, int begin, int end, int *cnt)
+constexpr int kBatch = 4;   // steps whose loads are in flight together
+
+// the lanes of the warp whose expert is this lane's (none for a dropped route): one vote for each bit of an expert's number
+__device__ __forceinline__ unsigned peers_of(int e, int bits)
 {
-    const int lane = threadIdx.x & 31;
-    for (int r0 = begin; r0 < end; r0 += 32) {
-        const int e = expert_of(a, r0 + lane);
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(peers) - 1) cnt[e] += __popc(peers);
-        __syncwarp();
+    unsigned m = __ballot_sync(0xffffffffu, e >= 0);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        if (b >= bits) break;
+        const bool one = e & (1 << b);
+        const unsigned v = __ballot_sync(0xffffffffu, one);
+        m &= one ? v : ~v;
+    }
+    return m;
+}
+
+// Counts of the segment [begin, end) into cnt[e * stride] (this warp's own), and rank[r] = earlier routes of the segment
+// with the same expert (nothing for a dropped route).
+__device__ __forceinline__ void count_segment(const SortArgs &a, int begin, int end, int *cnt, int stride, int *rank)
+{
+    const int lane = threadIdx.x & 31, bits = 32 - __clz(a.E - 1);
+    for (int r0 = begin; r0 < end; r0 += 32 * kBatch) {
+        int e[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) e[b] = r0 + 32 * b < end ? expert_of(a, r0 + 32 * b + lane) : -1;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (r0 + 32 * b >= end) break;
+            const unsigned peers = peers_of(e[b], bits);
+            const int lower = __popc(peers & ((1u << lane) - 1)), so_far = e[b] >= 0 ? cnt[e[b] * stride] : 0;
+            if (e[b] >= 0) rank[r0 + 32 * b + lane] = so_far + lower;
+            __syncwarp();
+            if (e[b] >= 0 && lower == 0) cnt[e[b] * stride] = so_far + __popc(peers);
+            __syncwarp();
+        }
     }
 }
 
-// place(r, row): row of every route of the segment (-1: dropped); next[e] = the warp's next row of e
+// place(r, row): row of every route of the segment (-1: dropped) = first[e] (the block's) + base[e * stride] (the warp's
+// among the block's) + rank
 template <class F>
-__device__ __forceinline__ void place_segment(const SortArgs &a, int begin, int end, int *next, F &&place)
+__device__ __forceinline__ void place_segment(const SortArgs &a, int begin, int end, const int *first, const int *base, int stride,
+                                              const int *rank, F &&place)
 {
     const int lane = threadIdx.x & 31;
-    for (int r0 = begin; r0 < end; r0 += 32) {
-        const int r = r0 + lane, e = expert_of(a, r);
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        const int row = e >= 0 ? next[e] + __popc(peers & ((1u << lane) - 1)) : -1;
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(peers) - 1) next[e] += __popc(peers);
-        __syncwarp();
-        if (r < a.n) place(r, row);
+    for (int r0 = begin; r0 < end; r0 += 32 * kBatch) {
+        int e[kBatch], k[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            e[b] = r0 + 32 * b < end ? expert_of(a, r0 + 32 * b + lane) : -1;
+            k[b] = e[b] >= 0 ? rank[r0 + 32 * b + lane] : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = r0 + 32 * b + lane;
+            if (r0 + 32 * b < end && r < a.n) place(r, e[b] >= 0 ? first[e[b]] + base[e[b] * stride] + k[b] : -1);
+        }
     }
 }
 
-// warp 0: exclusive scan of tot[E] into base[E + 1]
+// inclusive sum over the warp's lanes
+__device__ __forceinline__ int lane_scan(int v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// warp 0: exclusive scan of tot[E] into base[E + 1], 8 experts a lane (E <= 256)
 __device__ __forceinline__ void scan_experts(const int *tot, int *base, int E)
 {
     const int lane = threadIdx.x & 31;
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane, v = e < E ? tot[e] : 0;
-        int s = v;
+    int v[8], s = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
-        }
-        if (e < E) base[e] = carry + s - v;
-        carry += __shfl_sync(0xffffffffu, s, 31);
+    for (int i = 0; i < 8; ++i) {
+        v[i] = lane * 8 + i < E ? tot[lane * 8 + i] : 0;
+        s += v[i];
     }
-    if (lane == 0) base[E] = carry;
+    int at = lane_scan(s) - s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (lane * 8 + i < E) base[lane * 8 + i] = at;
+        at += v[i];
+    }
+    if (lane == 31) base[E] = at;
 }
 
-// per-warp counts -> each warp's first row within the block; tot[e] = the block's count
+// cnt[e * stride + w], the NW warps' counts -> each warp's first row of e within the block; tot[e] = the block's count.
+// A warp takes an expert, its lanes the warps' counts.
 template <int NW>
-__device__ __forceinline__ void scan_warps(int *cnt, int *tot, int E)
+__device__ __forceinline__ void scan_warps(int *cnt, int stride, int *tot, int E)
 {
-    for (int e = threadIdx.x; e < E; e += NW * 32) {
-        int s = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const int c = cnt[w * E + e];
-            cnt[w * E + e] = s;
-            s += c;
-        }
-        tot[e] = s;
+    const int lane = threadIdx.x & 31;
+    for (int e = threadIdx.x >> 5; e < E; e += NW) {
+        const int c = lane < NW ? cnt[e * stride + lane] : 0, s = lane_scan(c);
+        if (lane < NW) cnt[e * stride + lane] = s - c;
+        if (lane == 31) tot[e] = s;
     }
 }
 
 // The order of any number of routes, by one cluster of 1 to 8 blocks of 32 warps: at 16,384 routes
-// a warp walks two steps; at the largest, 4 M routes, the rows to be moved outweigh it by far.
-constexpr int kPlanWarps = 32;
+// a warp walks two steps; at the largest, 4 M routes, the rows to be moved outweigh it by far.  What it
+// takes is latency: two walks, two cluster barriers and the scans.
+constexpr int kPlanWarps = 32, kPlanStride = kPlanWarps + 1;   // 1: an expert's counts begin at another bank than the next one's
 
-__global__ void __launch_bounds__(kPlanWarps * 32) sort_plan_kernel(SortArgs a)
+// write_perm: else the copy kernel does it, where those scattered words spread over all SMs
+__global__ void __launch_bounds__(kPlanWarps * 32) sort_plan_kernel(SortArgs a, int write_perm)
 {
-    __shared__ int cnt[kPlanWarps * kMaxSortExperts];
-    __shared__ int tot[kMaxSortExperts], all[kMaxSortExperts], base[kMaxSortExperts + 1];
+    __shared__ int cnt[kPlanStride * kMaxSortExperts];
+    __shared__ int tot[kMaxSortExperts], all[kMaxSortExperts], first[kMaxSortExperts], base[kMaxSortExperts + 1];
     cg::cluster_group cl = cg::this_cluster();
     const int C = cl.num_blocks(), rank = cl.block_rank(), warp = threadIdx.x >> 5;
     griddep_launch_dependents();   // the copy of the rows waits for this kernel's end where it has to
@@ -122,40 +166,42 @@ __global__ void __launch_bounds__(kPlanWarps * 32) sort_plan_kernel(SortArgs a)
     const long b0 = static_cast<long>(rank * kPlanWarps + warp) * per;
     const int begin = static_cast<int>(b0 < a.n ? b0 : a.n);
     const int end = static_cast<int>(b0 + per < a.n ? b0 + per : a.n);
-    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += blockDim.x) cnt[i] = 0;
+    for (int i = threadIdx.x; i < kPlanStride * a.E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
-    count_segment(a, begin, end, cnt + warp * a.E);
+    count_segment(a, begin, end, cnt + warp, kPlanStride, a.slot);   // ranks where the rows will stand
     __syncthreads();
-    scan_warps<kPlanWarps>(cnt, tot, a.E);
+    scan_warps<kPlanWarps>(cnt, kPlanStride, tot, a.E);
     cl.sync();
-    // the cluster's counts, and those of the blocks before this one
-    int before = 0;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {   // E <= blockDim.x: one turn
-        int sum = 0;
-        for (int c = 0; c < C; ++c) {
-            const int v = cl.map_shared_rank(tot, c)[e];
-            before += c < rank ? v : 0;
-            sum += v;
+    // The cluster's counts of every expert, and those of the blocks before this one: a thread takes
+    // an expert and one of eight blocks.
+    for (int i = threadIdx.x; i < kMaxSortExperts * 8; i += blockDim.x) {
+        const int e = i >> 3, c = i & 7, v = e < a.E && c < C ? cl.map_shared_rank(tot, c)[e] : 0;
+        int sum = v, before = c < rank ? v : 0;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
         }
-        all[e] = sum;
+        if (c == 0 && e < a.E) {
+            all[e] = sum;
+            first[e] = before;
+        }
     }
-    cl.sync();   // no block reads another's counts, or ends, after this
+    cl.barrier_arrive();           // this block has read the others' counts
+    __syncthreads();
     if (warp == 0) scan_experts(all, base, a.E);
     __syncthreads();
-    if (threadIdx.x < a.E) {
-        const int first = base[threadIdx.x] + before;
-#pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) cnt[w * a.E + threadIdx.x] += first;
-    }
+    if (threadIdx.x < a.E) first[threadIdx.x] += base[threadIdx.x];   // this block's first row of the expert
     if (rank == 0)
         for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = base[e];
     __syncthreads();
-    place_segment(a, begin, end, cnt + warp * a.E, [&](int r, int row) {
+    place_segment(a, begin, end, first, cnt + warp, kPlanStride, a.slot, [&](int r, int row) {
         a.slot[r] = row;
-        if (row >= 0) a.perm[row] = r;
+        if (write_perm && row >= 0) a.perm[row] = r;
     });
     for (int r = base[a.E] + rank * static_cast<int>(blockDim.x) + threadIdx.x; r < a.n; r += C * blockDim.x)
         a.perm[r] = -1;   // behind the last row
+    cl.barrier_wait();             // no block ends while another reads its counts
 }
 
 // ---- the rows --------------------------------------------------------------------
@@ -180,8 +226,9 @@ struct CopyArgs {
     long units;                 // T * upr
 };
 
+// perm: nullptr, or where the first unit of a token notes its routes
 template <class V, class S>
-__device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long unit, S &&slot_of, bool wait)
+__device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long unit, S &&slot_of, bool wait, int *perm)
 {
     const int lanes = 1 << c.lg, lane = threadIdx.x & (lanes - 1);
     const bool on = unit < c.units;
@@ -194,53 +241,54 @@ __device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long 
         if (v0 + u * lanes < c.vpr) v[u] = __ldg(src + v0 + u * lanes);
     if (wait) griddep_wait();   // x was there before the call; the slots are the previous kernel's
     if (!on) return;
-    for (int j = 0; j < k; ++j) {
-        const int row = slot_of(t * k + j);
-        if (row < 0 || row >= n) continue;
-        V *dst = static_cast<V *>(c.rows) + static_cast<size_t>(row) * c.vpr;
+    for (int j0 = 0; j0 < k; j0 += kUnroll) {
+        int row[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (v0 + u * lanes < c.vpr) dst[v0 + u * lanes] = v[u];
+        for (int j = 0; j < kUnroll; ++j) row[j] = j0 + j < k ? slot_of(t * k + j0 + j) : -1;
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+            if (row[j] < 0 || row[j] >= n) continue;
+            if (perm && v0 == j) perm[row[j]] = t * k + j0 + j;   // a lane each
+            V *dst = static_cast<V *>(c.rows) + static_cast<size_t>(row[j]) * c.vpr;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (v0 + u * lanes < c.vpr) dst[v0 + u * lanes] = v[u];
+        }
     }
 }
 
 template <class V>
-__global__ void __launch_bounds__(256) sort_copy_kernel(CopyArgs c, const int *slot, int k, int n)
+__global__ void __launch_bounds__(256) sort_copy_kernel(CopyArgs c, const int *slot, int k, int n, int *perm)
 {
     const long unit = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) >> c.lg;
     // plain loads: the slots are written while this kernel may already run
-    copy_unit<V>(c, k, n, unit, [&](int r) { return *reinterpret_cast<const volatile int *>(slot + r); }, true);
+    copy_unit<V>(c, k, n, unit, [&](int r) { return *reinterpret_cast<const volatile int *>(slot + r); }, true, perm);
 }
 
 // A small batch in one launch: every block finds the whole order by itself (it is a few steps of
 // eight warps) and copies its share of the rows; block 0 writes the order out.
-constexpr int kSmallWarps = 8;
+constexpr int kSmallWarps = 8, kSmallStride = kSmallWarps + 1;
 constexpr int kSmallRoutes = 1024;
 
 template <class V>
 __global__ void __launch_bounds__(kSmallWarps * 32) sort_small_kernel(SortArgs a, CopyArgs c)
 {
-    __shared__ int cnt[kSmallWarps * kMaxSortExperts];
+    __shared__ int cnt[kSmallStride * kMaxSortExperts];
     __shared__ int tot[kMaxSortExperts], base[kMaxSortExperts + 1];
     __shared__ int slots[kSmallRoutes];
     const int warp = threadIdx.x >> 5;
     const int per = ((a.n + kSmallWarps - 1) / kSmallWarps + 31) / 32 * 32;
     const int begin = min(warp * per, a.n), end = min(begin + per, a.n);
-    for (int i = threadIdx.x; i < kSmallWarps * a.E; i += blockDim.x) cnt[i] = 0;
+    for (int i = threadIdx.x; i < kSmallStride * a.E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
-    count_segment(a, begin, end, cnt + warp * a.E);
+    count_segment(a, begin, end, cnt + warp, kSmallStride, slots);
     __syncthreads();
-    scan_warps<kSmallWarps>(cnt, tot, a.E);
+    scan_warps<kSmallWarps>(cnt, kSmallStride, tot, a.E);
     __syncthreads();
     if (warp == 0) scan_experts(tot, base, a.E);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-#pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) cnt[w * a.E + e] += base[e];
-    }
-    __syncthreads();
     const bool first = blockIdx.x == 0;
-    place_segment(a, begin, end, cnt + warp * a.E, [&](int r, int row) {
+    place_segment(a, begin, end, base, cnt + warp, kSmallStride, slots, [&](int r, int row) {
         slots[r] = row;
         if (first) {
             a.slot[r] = row;
@@ -254,7 +302,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) sort_small_kernel(SortArgs a
     __syncthreads();
     if (!c.x) return;
     const long unit = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) >> c.lg;
-    copy_unit<V>(c, a.k, a.n, unit, [&](int r) { return slots[r]; }, false);
+    copy_unit<V>(c, a.k, a.n, unit, [&](int r) { return slots[r]; }, false, nullptr);
 }
 
 // lanes of a unit and units of a row for rows of vpr vectors: short rows share a warp
@@ -273,20 +321,19 @@ cudaError_t launch_sort(const SortArgs &a, const void *x, void *rows, size_t row
     const unsigned grid = static_cast<unsigned>(((c.units << c.lg) + 255) / 256);
     if (a.n <= kSmallRoutes)
         return op_launch(sort_small_kernel<V>, dim3(x ? grid : 1), dim3(kSmallWarps * 32), 0, s, false, 1, a, c);
-    // one block for up to 4 steps a warp, then as many as the cluster takes
-    const int cluster = a.n <= 4096 ? 1 : a.n <= 8192 ? 2 : a.n <= 16384 ? 4 : 8;
-    cudaError_t e = op_launch(sort_plan_kernel, dim3(cluster), dim3(kPlanWarps * 32), 0, s, false, cluster, a);
+    // one step a warp as far as the cluster goes
+    const int cluster = a.n <= 2048 ? 2 : a.n <= 4096 ? 4 : 8;
+    cudaError_t e = op_launch(sort_plan_kernel, dim3(cluster), dim3(kPlanWarps * 32), 0, s, false, cluster, a, x ? 0 : 1);
     if (e != cudaSuccess || !x) return e;
     return op_launch(sort_copy_kernel<V>, dim3(grid), dim3(256), 0, s, true, 1, c, static_cast<const int *>(a.slot), a.k,
-                     a.n);
+                     a.n, a.perm);
 }
 
 // ---- back, with the gates applied ---------------------------------------------------
 //
-// One thread forms N consecutive elements of out[t]: fp32 products summed in pick order, one
-// rounding at the end.  A dropped route adds nothing, whatever its gate holds.
-
-constexpr int kGroup = 4;   // picks handled together
+// nt threads take a token; a thread forms kSteps vectors of out[t] at a time, with the picks' rows of a group of G in
+// flight together: fp32 products summed in pick order, one rounding at the end.  A dropped route adds
+// nothing, whatever its gate holds.
 
 struct UnsortArgs {
     int T, k, d;
@@ -296,45 +343,75 @@ struct UnsortArgs {
     void *out;
 };
 
-template <class R, class O, int N>
-__global__ void __launch_bounds__(256) unsort_kernel(UnsortArgs a, int vpr, long items)
+// first elements of the rows of picks j0 .. j0 + G - 1 of token t (-1: a dropped route), and their gates
+template <int G>
+__device__ __forceinline__ void picks_of(const int *slot, const float *gate, int t, int k, int j0, int n, int d, long (&at)[G],
+                                         float (&g)[G])
 {
-    const int n = a.T * a.k;
-    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= items) return;
-    const int t = row_of(i, vpr, items), c = static_cast<int>(i - static_cast<long>(t) * vpr) * N;
-    const R *rows = static_cast<const R *>(a.rows) + c;
-    float acc[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-        // the loads of a group of picks are in flight together
-        int row[kGroup];
-        float g[kGroup];
-        Raw<R, N> v[kGroup];
+    for (int j = 0; j < G; ++j) {
+        const int row = j0 + j < k ? __ldg(slot + t * k + j0 + j) : -1;
+        const bool on = row >= 0 && row < n;
+        at[j] = on ? static_cast<long>(row) * d : -1;
+        g[j] = on && gate ? __ldg(gate + t * k + j0 + j) : 1.f;
+    }
+}
+
+// steps that keep about `bytes` a thread in flight
+constexpr int steps_of(int step_bytes, int bytes) { return step_bytes * 8 <= bytes ? 8 : step_bytes * 4 <= bytes ? 4 : step_bytes * 3 <= bytes ? 3 : 2; }
+
+template <class R, int N, int G> constexpr int unsort_steps() { return steps_of(N * G * static_cast<int>(sizeof(R)), 64); }
+
+// NT: nt where it is fixed (the steps are then at constant distances), else 0
+template <class R, class O, int N, int G, int NT>
+__global__ void __launch_bounds__(256) unsort_kernel(UnsortArgs a, int threads)
+{
+    const int nt = NT ? NT : threads;
+    constexpr int kSteps = unsort_steps<R, N, G>();
+    const int n = a.T * a.k, sub = static_cast<int>(threadIdx.x) / nt, lane = static_cast<int>(threadIdx.x) - sub * nt;
+    const int t = blockIdx.x * (blockDim.x / nt) + sub;
+    if (t >= a.T) return;
+    O *out = static_cast<O *>(a.out) + static_cast<size_t>(t) * a.d;
+    const R *rows = static_cast<const R *>(a.rows);
+    long at[G];
+    float g[G];
+    if (a.k <= G) picks_of<G>(a.slot, a.gate, t, a.k, 0, n, a.d, at, g);
+    for (int c0 = lane * N; c0 < a.d; c0 += nt * N * kSteps) {
+        float acc[kSteps][N];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            row[j] = j0 + j < a.k ? __ldg(a.slot + t * a.k + j0 + j) : -1;
-            g[j] = a.gate && j0 + j < a.k ? __ldg(a.gate + t * a.k + j0 + j) : 1.f;
+        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[u][e] = 0.f;
+        for (int j0 = 0; j0 < a.k; j0 += G) {
+            if (a.k > G) picks_of<G>(a.slot, a.gate, t, a.k, j0, n, a.d, at, g);
+            Raw<R, N> v[kSteps][G];
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    if (at[j] >= 0 && c0 + u * nt * N < a.d) v[u][j].load(rows + at[j] + c0 + u * nt * N);
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    if (at[j] >= 0 && c0 + u * nt * N < a.d) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[u][e] = fmaf(g[j], v[u][j].get(e), acc[u][e]);
+                    }
         }
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            if (row[j] >= 0 && row[j] < n) v[j].load(rows + static_cast<size_t>(row[j]) * a.d);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            if (row[j] >= 0 && row[j] < n) {
-#pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] = fmaf(g[j], v[j].get(e), acc[e]);
-            }
+        for (int u = 0; u < kSteps; ++u) {
+            if (c0 + u * nt * N >= a.d) continue;
+            Raw<O, N> o;
+            o.set([&](int e) { return acc[u][e]; });
+            o.store(out + c0 + u * nt * N);
+        }
     }
-    Raw<O, N> o;
-    o.set([&](int e) { return acc[e]; });
-    o.store(static_cast<O *>(a.out) + static_cast<size_t>(t) * a.d + c);
 }
 
 // ---- the gradient of the way back -----------------------------------------------------
 //
-// NT threads take a token.  For a group of G picks a thread has kSteps vectors of dout[t] and of every
+// nt threads, whole warps, take a token.  For a group of G picks a thread has kSteps vectors of dout[t] and of every
 // pick's row in flight together (more picks read dout[t] again, from the caches); it writes the
 // picks' gradient rows and adds up the products for the gates' gradients in fp32, joined over
 // the threads in a fixed tree.
@@ -348,58 +425,52 @@ struct UnsortGradArgs {
     float *dgate;               // nullptr: not wanted
 };
 
+template <class R, class O, int N, int G>
+constexpr int unsort_grad_steps() { return steps_of(N * static_cast<int>(sizeof(O) + G * sizeof(R)), 96); }
+
 template <class R, class O, int N, int G, int NT>
-__global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a)
+__global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a, int threads)
 {
-    constexpr int kTokens = 256 / NT, kWarps = NT / 32;
-    // vectors of a row in flight: about 192 bytes a thread
-    constexpr int kBytes = N * static_cast<int>(sizeof(O) + G * sizeof(R));
-    constexpr int kSteps = kBytes >= 96 ? 2 : kBytes >= 48 ? 3 : kBytes >= 20 ? 4 : 8;
-    __shared__ float red[2][kTokens * kWarps][G];
-    const int n = a.T * a.k, lane = threadIdx.x % NT, sub = threadIdx.x / NT;
-    const int t = blockIdx.x * kTokens + sub;
-    if (NT == 32 && t >= a.T) return;   // NT == 256: the grid is T blocks
+    const int nt = NT ? NT : threads;
+    constexpr int kSteps = unsort_grad_steps<R, O, N, G>();
+    __shared__ float red[2][8][G];
+    const int n = a.T * a.k, sub = static_cast<int>(threadIdx.x) / nt, lane = static_cast<int>(threadIdx.x) - sub * nt;
+    const int last = blockIdx.x * (blockDim.x / nt) + sub, t = min(last, a.T - 1), warps = nt / 32;
+    const bool real = last < a.T;   // else: only at the barriers
     const O *dout = static_cast<const O *>(a.dout) + static_cast<size_t>(t) * a.d;
+    const R *rows = static_cast<const R *>(a.rows);
+    R *drows = static_cast<R *>(a.drows);
     int parity = 0;
     for (int j0 = 0; j0 < a.k; j0 += G) {
-        bool on[G];
-        const R *src[G];
-        R *dst[G];
+        long at[G];
         float g[G], dot[G];
+        picks_of<G>(a.slot, a.gate, t, a.k, j0, real ? n : 0, a.d, at, g);
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int row = j0 + j < a.k ? __ldg(a.slot + t * a.k + j0 + j) : -1;
-            on[j] = row >= 0 && row < n;
-            const size_t at = on[j] ? static_cast<size_t>(row) * a.d : 0;
-            src[j] = static_cast<const R *>(a.rows) + at;
-            dst[j] = static_cast<R *>(a.drows) + at;
-            g[j] = on[j] && a.gate ? __ldg(a.gate + t * a.k + j0 + j) : 1.f;
-            dot[j] = 0.f;
-        }
-        for (int c0 = lane * N; c0 < a.d; c0 += NT * N * kSteps) {
+        for (int j = 0; j < G; ++j) dot[j] = 0.f;
+        for (int c0 = real ? lane * N : a.d; c0 < a.d; c0 += nt * N * kSteps) {
             Raw<O, N> dv[kSteps];
             Raw<R, N> rv[kSteps][G];
 #pragma unroll
             for (int u = 0; u < kSteps; ++u) {
-                const int c = c0 + u * NT * N;
+                const int c = c0 + u * nt * N;
                 if (c >= a.d) continue;
                 dv[u].load(dout + c);
                 if (a.dgate) {
 #pragma unroll
                     for (int j = 0; j < G; ++j)
-                        if (on[j]) rv[u][j].load(src[j] + c);
+                        if (at[j] >= 0) rv[u][j].load(rows + at[j] + c);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kSteps; ++u) {
-                const int c = c0 + u * NT * N;
+                const int c = c0 + u * nt * N;
                 if (c >= a.d) continue;
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    if (!on[j]) continue;
+                    if (at[j] < 0) continue;
                     Raw<R, N> o;
                     o.set([&](int e) { return g[j] * dv[u].get(e); });
-                    o.store(dst[j] + c);
+                    o.store(drows + at[j] + c);
                     if (a.dgate) {
 #pragma unroll
                         for (int e = 0; e < N; ++e) dot[j] = fmaf(dv[u].get(e), rv[u][j].get(e), dot[j]);
@@ -410,10 +481,10 @@ __global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a)
         if (!a.dgate) continue;
 #pragma unroll
         for (int j = 0; j < G; ++j) dot[j] = warp_sum(dot[j]);
-        if constexpr (NT == 32) {
+        if (nt == 32) {
 #pragma unroll
             for (int j = 0; j < G; ++j)
-                if (lane == j && j0 + j < a.k) a.dgate[t * a.k + j0 + j] = dot[j];
+                if (lane == j && real && j0 + j < a.k) a.dgate[t * a.k + j0 + j] = dot[j];   // 0 for a dropped route
         } else {
             // two buffers by turns: one barrier a group
             if ((threadIdx.x & 31) == 0) {
@@ -421,35 +492,65 @@ __global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a)
                 for (int j = 0; j < G; ++j) red[parity][threadIdx.x >> 5][j] = dot[j];
             }
             __syncthreads();
-            if (lane < G && j0 + lane < a.k) {
+            if (lane < G && real && j0 + lane < a.k) {
                 float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += red[parity][w][lane];
-                a.dgate[t * a.k + j0 + lane] = s;   // 0 for a dropped route
+                for (int w = 0; w < warps; ++w) s += red[parity][sub * warps + w][lane];
+                a.dgate[t * a.k + j0 + lane] = s;
             }
             parity ^= 1;
         }
     }
 }
 
+// Threads of a token for rows of `vecs` vectors, `steps` at a time.  16-byte vectors: as few threads as fill the row
+// in as many rounds as 256 would take (a multiple of `unit`), which leaves none idle.  Narrower ones:
+// 256 threads (or a warp for short rows), since their loads are what there is too few of in flight.
+// A block holds as many tokens as make up 256 threads.
+struct TokenShape {
+    int nt, block, grid;
+};
+
+TokenShape token_shape(int T, int vecs, int steps, int unit, bool narrow)
+{
+    const int rounds = (vecs + 256 * steps - 1) / (256 * steps), per = (vecs + rounds * steps - 1) / (rounds * steps);
+    TokenShape s;
+    s.nt = narrow ? (vecs <= 128 ? 32 : 256) : (per + unit - 1) / unit * unit;
+    const int tokens = 256 / s.nt;
+    s.block = tokens * s.nt;
+    s.grid = (T + tokens - 1) / tokens;
+    return s;
+}
+
+template <class R, class O, int N, int G>
+cudaError_t launch_unsort_group(const UnsortArgs &a, cudaStream_t s)
+{
+    const TokenShape sh = token_shape(a.T, a.d / N, unsort_steps<R, N, G>(), 8, N <= 2);
+    void (*kernel)(UnsortArgs, int);
+    if constexpr (N > 2) kernel = unsort_kernel<R, O, N, G, 0>;
+    else kernel = sh.nt == 32 ? unsort_kernel<R, O, N, G, 32> : unsort_kernel<R, O, N, G, 256>;
+    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, false, 1, a, sh.nt);
+}
+
 template <class R, class O, int N>
 cudaError_t launch_unsort(const UnsortArgs &a, cudaStream_t s)
 {
-    const int vpr = a.d / N;
-    const long items = static_cast<long>(a.T) * vpr;
-    return op_launch(unsort_kernel<R, O, N>, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, s, false, 1,
-                     a, vpr, items);
+    return a.k <= 2 ? launch_unsort_group<R, O, N, 2>(a, s) : launch_unsort_group<R, O, N, 4>(a, s);
+}
+
+template <class R, class O, int N, int G>
+cudaError_t launch_unsort_grad_group(const UnsortGradArgs &a, cudaStream_t s)
+{
+    const TokenShape sh = token_shape(a.T, a.d / N, unsort_grad_steps<R, O, N, G>(), 32, N <= 2);
+    void (*kernel)(UnsortGradArgs, int);
+    if constexpr (N > 2) kernel = unsort_grad_kernel<R, O, N, G, 0>;
+    else kernel = sh.nt == 32 ? unsort_grad_kernel<R, O, N, G, 32> : unsort_grad_kernel<R, O, N, G, 256>;
+    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, false, 1, a, sh.nt);
 }
 
 template <class R, class O, int N>
 cudaError_t launch_unsort_grad(const UnsortGradArgs &a, cudaStream_t s)
 {
-    const dim3 grid(a.d / N <= 128 ? (a.T + 7) / 8 : a.T);   // a warp covers 128 vectors in a few steps
-    if (a.k <= 2)
-        return op_launch(a.d / N <= 128 ? unsort_grad_kernel<R, O, N, 2, 32> : unsort_grad_kernel<R, O, N, 2, 256>, grid,
-                         dim3(256), 0, s, false, 1, a);
-    return op_launch(a.d / N <= 128 ? unsort_grad_kernel<R, O, N, 4, 32> : unsort_grad_kernel<R, O, N, 4, 256>, grid,
-                     dim3(256), 0, s, false, 1, a);
+    return a.k <= 2 ? launch_unsort_grad_group<R, O, N, 2>(a, s) : launch_unsort_grad_group<R, O, N, 4>(a, s);
 }
 
 // the vector width by the row width: 16 bytes of the wider type's neighbour where d allows
