@@ -134,13 +134,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t p)
     return v;
 }
 
-// (w & mask) | bits in one instruction: both constants come from registers
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
-{
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(bits));
-    return v;
-}
 template <class T2>
 __device__ __forceinline__ uint32_t bits_of(const T2 &v)
 {
@@ -156,30 +149,30 @@ __device__ __forceinline__ T2 as16(uint32_t w)
     return v;
 }
 
-// The four operand pairs of a word of 4-bit values: five integer operations and four 16-bit FMAs for
-// eight weights (the integer pipe is the one that limits this kernel, so the FMAs do what they can).
-//
-// bf16: an integer v below 256 in the low byte of a half is the bf16 v * 2^-133, on both sides of
-// the smallest normal number.  A mask leaves u or 16 u there (u = value + 8), and an exact FMA makes
-// (u - 8) / 128 of it; the joined sums are taken 128 times.
-// fp16: the same bits OR-ed into 1024, whose last place is 1, are 1024 + u and 1024 + 16 u; an exact
-// FMA makes u - 8.
+// The four operand pairs of a word of 4-bit values u = value + 8.  The integer and FMA pipes limit this kernel, not
+// the tensor cores, so the fast form is a mask per pair: an integer v below 256 in the low byte of a half is the
+// 16-bit float v * kTiny, on both sides of the smallest normal number of bf16 (2^-133) and among
+// the subnormal ones of fp16 (2^-24).  Odd pairs, the features g + 8, hold 16 u.  The products' sums are
+// then those of u, and -8 times the sum of the group's inputs, with which the accumulators start, makes them
+// those of u - 8; the scale's factor takes the powers of two back.  bf16 inputs are staged at 2^100 times their
+// value, which keeps the products in the normal range.  A phase whose inputs do not allow that (bf16 from 2^27 up,
+// inf, nan) takes the exact form: an FMA per pair makes u - 8 of it, as an ordinary number.
+// At 16 rows over 8 experts of 6144 x 32768, gated: 307 us with the FMAs everywhere.
 template <class T> struct Deq;
 template <> struct Deq<__nv_bfloat16> {
-    static constexpr float kScale = 128.f;
-    __nv_bfloat162 lo, hi, off;
-    uint32_t m0, m1;
-    __device__ __forceinline__ Deq()
-        : lo(__floats2bfloat162_rn(0x1p126f, 0x1p126f)), hi(__floats2bfloat162_rn(0x1p122f, 0x1p122f)),
-          off(__floats2bfloat162_rn(-0.0625f, -0.0625f)), m0(0x000f000fu), m1(0x00f000f0u)
+    static constexpr float kFast[2] = {0x1p33f, 0x1p29f};      // 2^133 / 2^100, and / 16
+    static constexpr float kExact = 128.f;                     // operands are (u - 8) / 128
+    static constexpr float kStart = -0x1p-30f;                 // -8 * 2^-133 * 2^100
+    static constexpr uint32_t kLimit = 0x4d00;                 // 2^27, as bits
+    static __device__ __forceinline__ uint32_t stage(uint32_t w)
     {
+        return pack2<__nv_bfloat16>(__uint_as_float(w << 16) * 0x1p100f, __uint_as_float(w & 0xffff0000u) * 0x1p100f);
     }
-    __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) const
+    static __device__ __forceinline__ float sum2(uint32_t w) { return __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u); }
+    static __device__ __forceinline__ uint32_t exact(uint32_t v, int odd)
     {
-        const uint32_t h = w >> 8;
-        const uint32_t v[4] = {w & m0, w & m1, h & m0, h & m1};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = bits_of(__hfma2(as16<__nv_bfloat162>(v[i]), i & 1 ? hi : lo, off));
+        const float f = odd ? 0x1p122f : 0x1p126f;
+        return bits_of(__hfma2(as16<__nv_bfloat162>(v), __floats2bfloat162_rn(f, f), __floats2bfloat162_rn(-0.0625f, -0.0625f)));
     }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
@@ -190,20 +183,21 @@ template <> struct Deq<__nv_bfloat16> {
     }
 };
 template <> struct Deq<__half> {
-    static constexpr float kScale = 1.f;
-    __half2 lo, hi, off, offhi;
-    uint32_t m0, m1, one;
-    __device__ __forceinline__ Deq()
-        : lo(__floats2half2_rn(1.f, 1.f)), hi(__floats2half2_rn(0.0625f, 0.0625f)), off(__floats2half2_rn(-1032.f, -1032.f)),
-          offhi(__floats2half2_rn(-72.f, -72.f)), m0(0x000f000fu), m1(0x00f000f0u), one(0x64006400u)
+    static constexpr float kFast[2] = {0x1p24f, 0x1p20f};
+    static constexpr float kExact = 1.f;
+    static constexpr float kStart = -0x1p-21f;                 // -8 * 2^-24
+    static constexpr uint32_t kLimit = 0x7c00;                 // inf
+    static __device__ __forceinline__ uint32_t stage(uint32_t w) { return w; }
+    static __device__ __forceinline__ float sum2(uint32_t w)
     {
+        const float2 f = __half22float2(as16<__half2>(w));
+        return f.x + f.y;
     }
-    __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) const
+    // OR-ed into 1024, whose last place is 1: 1024 + u, 1024 + 16 u
+    static __device__ __forceinline__ uint32_t exact(uint32_t v, int odd)
     {
-        const uint32_t h = w >> 8;
-        const uint32_t v[4] = {and_or(w, m0, one), and_or(w, m1, one), and_or(h, m0, one), and_or(h, m1, one)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = bits_of(__hfma2(as16<__half2>(v[i]), i & 1 ? hi : lo, i & 1 ? offhi : off));
+        const float f = odd ? 0.0625f : 1.f, o = odd ? -72.f : -1032.f;
+        return bits_of(__hfma2(as16<__half2>(v | 0x64006400u), __floats2half2_rn(f, f), __floats2half2_rn(o, o)));
     }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
@@ -214,30 +208,141 @@ template <> struct Deq<__half> {
     }
 };
 
-// x rows [row0, row0 + rows) at inputs [k0, k0 + nk) into shared memory, in the order in which a lane takes its
-// operands: within 64 inputs, input 16 j + 4 c + i at place 16 c + 4 j + i.  Inputs behind K are 0 (the
-// weights there are too, but 0 times what the memory holds need not be).
-__device__ __forceinline__ void stage_x(const W4Args &a, char *xs, int stride, int row0, int rows, int k0, int nk)
-{
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
-    const int per_row = nk / 8;
-    for (int p = threadIdx.x; p < rows * per_row; p += kWarps * 32) {
-        const int r = p / per_row, kk = (p - r * per_row) * 8, k = k0 + kk;
-        const uint16_t *src = x + static_cast<size_t>(row0 + r) * a.K + k;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if ((a.K & 7) == 0) {
-            if (k < a.K) v = __ldg(reinterpret_cast<const uint4 *>(src));
-        } else {
-            uint16_t h[8];
+// x rows [row0, row0 + rows) at inputs [k0, k0 + nk), PU units at most, on their way into shared memory in the order in
+// which a lane takes its operands: within 64 inputs, input 16 j + 4 c + i at place 16 c + 4 j + i.  Inputs behind K
+// are 0 (the weights there are too, but 0 times what the memory holds need not be).  The loads are all in flight
+// together, before the barrier that frees the place.
+template <class T, int G, int NB, int PU>
+struct StageX {
+    static constexpr int kPer = PU * kUnitK / 8, kPieces = 8 * NB * kPer / (kWarps * 32);   // 16-byte pieces: a row's, a thread's
+    uint4 v[kPieces];
+    __device__ __forceinline__ void load(const W4Args &a, int row0, int rows, int k0, int nk)
+    {
+        const uint16_t *x = static_cast<const uint16_t *>(a.x) + static_cast<size_t>(row0) * a.K;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = k + i < a.K ? __ldg(src + i) : static_cast<uint16_t>(0);
-            v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = threadIdx.x + i * (kWarps * 32), r = p / kPer, kk = p % kPer * 8, k = k0 + kk;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r >= rows || kk >= nk || k >= a.K) continue;
+            const uint16_t *src = x + static_cast<size_t>(r) * a.K + k;
+            if ((a.K & 7) == 0) {
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = k + e < a.K ? __ldg(src + e) : 0u;
+                v[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+            }
         }
-        const int j = (kk >> 4) & 3, c = (kk >> 2) & 3;   // c is 0 or 2
-        char *dst = xs + r * stride + (kk >> 6) * 128 + c * 32 + j * 8;
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(v.x, v.y);
-        *reinterpret_cast<uint2 *>(dst + 32) = make_uint2(v.z, v.w);
     }
+    // an input that the fast form cannot take
+    __device__ __forceinline__ bool beyond() const
+    {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+        }
+        return (most & 0xffffu) >= Deq<T>::kLimit || (most >> 16) >= Deq<T>::kLimit;
+    }
+    // The inputs, and (fast) what the accumulators of each group and row start with: the pieces of a group are
+    // those of G / 8 neighbouring lanes.  Rows behind the last one stay as they are: a product's column is its row's own.
+    __device__ __forceinline__ void store(char *xs, int stride, float *starts, int rows, bool fast) const
+    {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = threadIdx.x + i * (kWarps * 32), r = p / kPer, kk = p % kPer * 8;
+            if (r >= rows) continue;                          // whole warps: a row has at least 64 pieces
+            const int j = (kk >> 4) & 3, c = (kk >> 2) & 3;   // c is 0 or 2
+            char *dst = xs + r * stride + (kk >> 6) * 128 + c * 32 + j * 8;
+            uint4 u = v[i];
+            if (fast) {
+                float sum = Deq<T>::sum2(u.x) + Deq<T>::sum2(u.y) + (Deq<T>::sum2(u.z) + Deq<T>::sum2(u.w));
+#pragma unroll
+                for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (kk % G == 0) starts[kk / G * (8 * NB) + r] = sum * Deq<T>::kStart;
+                u = make_uint4(Deq<T>::stage(u.x), Deq<T>::stage(u.y), Deq<T>::stage(u.z), Deq<T>::stage(u.w));
+            }
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(u.x, u.y);
+            *reinterpret_cast<uint2 *>(dst + 32) = make_uint2(u.z, u.w);
+        }
+    }
+};
+
+// One unit of a feature block: two chunks of 64 inputs, two feature tiles.  st: its stage, xu: the lane's inputs,
+// start: the lane's pair of rows' starting values of the unit's first group.
+template <class T, int G, int NB, bool FAST>
+__device__ __forceinline__ void w4_unit(float (&acc)[2][NB][4], uint32_t st, uint32_t xu, int xrows, uint32_t start)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    float part[2][NB][4];
+    auto begin = [&](int group) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float v0 = 0.f, v1 = 0.f;
+            if (FAST)
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v0), "=f"(v1) : "r"(start + (group * NB + nb) * 32));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                part[t][nb][0] = v0;
+                part[t][nb][1] = v1;
+                part[t][nb][2] = v0 * 16.f;
+                part[t][nb][3] = v1 * 16.f;
+            }
+        }
+    };
+    // the group's sums times its scales: features g, g + 8, g + 16, g + 24
+    auto flush = [&](int group) {
+        uint32_t lo, hi;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(st + kUnitBytes + group * 64 + g * 8));
+        const float f0 = FAST ? Deq<T>::kFast[0] : Deq<T>::kExact, f1 = FAST ? Deq<T>::kFast[1] : Deq<T>::kExact;
+        const float s[4] = {__uint_as_float(lo << 16) * f0, __uint_as_float(lo & 0xffff0000u) * f1, __uint_as_float(hi << 16) * f0,
+                            __uint_as_float(hi & 0xffff0000u) * f1};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][nb][i] = fmaf(s[2 * t + (i >> 1)], part[t][nb][i], acc[t][nb][i]);
+    };
+    begin(0);
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+        uint4 w[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) w[t] = lds128(st + (ch * 2 + t) * 512 + lane * 16);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {        // two steps of 16 inputs
+            uint4 xv[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) xv[nb] = lds128(xu + nb * xrows + ch * 128 + half * 16);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t v = half ? (j ? w[t].w : w[t].z) : (j ? w[t].y : w[t].x), h = v >> 8;
+                    uint32_t av[4] = {v & 0x000f000fu, v & 0x00f000f0u, h & 0x000f000fu, h & 0x00f000f0u};
+                    if (!FAST) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) av[i] = Deq<T>::exact(av[i], i & 1);
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        Deq<T>::mma(part[t][nb], av, j ? xv[nb].z : xv[nb].x, j ? xv[nb].w : xv[nb].y);
+                }
+            if (G == 32) {
+                flush(ch * 2 + half);
+                if (ch * 2 + half < 3) begin(ch * 2 + half + 1);
+            }
+        }
+        if (G == 64) {
+            flush(ch);
+            if (ch == 0) begin(1);
+        }
+    }
+    if (G == 128) flush(0);
 }
 
 __device__ __forceinline__ float gelu_of(float a)
@@ -271,9 +376,9 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
 
     char *xs = smem + kWarps * kStages * kStageBytes;
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
-    const uint32_t xaddr = smem_u32(xs) + g * kXStride + c * 32;
+    float *starts = reinterpret_cast<float *>(xs + 8 * NB * kXStride);
+    const uint32_t xaddr = smem_u32(xs) + g * kXStride + c * 32, saddr = smem_u32(starts) + c * 8;
 
-    const Deq<T> deq;
     float acc[2][NB][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -282,27 +387,35 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
 
-    int next = u0 + kpart, put = 0;                           // next unit to copy, its stage
+    int left = on && u0 + kpart < u1 ? (u1 - u0 - kpart + a.kparts - 1) / a.kparts : 0, put = 0;   // units to copy, the next one's stage
+    const uint8_t *wnext = wsrc + static_cast<size_t>(u0 + kpart) * kUnitBytes;
+    const uint8_t *snext = ssrc + static_cast<size_t>(u0 + kpart) * (kGroups * 64);
+    const int wstep = a.kparts * kUnitBytes, sstep = a.kparts * (kGroups * 64);
+    const uint32_t to = ring + lane * 16;
     auto issue = [&]() {
-        if (on && next < u1) {
-            const uint32_t dst = ring + put * kStageBytes + lane * 16;
-            const uint8_t *s = wsrc + static_cast<size_t>(next) * kUnitBytes;
+        if (left > 0) {
+            const uint32_t dst = to + put * kStageBytes;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cp16(dst + i * 512, s + i * 512);
-            if (lane < 4 * kGroups) cp16(dst + kUnitBytes, ssrc + static_cast<size_t>(next) * (kGroups * 64));
+            for (int i = 0; i < 4; ++i) cp16(dst + i * 512, wnext + i * 512);
+            if (lane < 4 * kGroups) cp16(dst + kUnitBytes, snext);
         }
         cp_commit();
-        next += a.kparts;
+        --left;
+        wnext += wstep;
+        snext += sstep;
         put = put + 1 == kStages ? 0 : put + 1;
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
+    griddep_wait();                                           // x and the rows of y; the weights are nobody's output
 
     int get = 0, u = u0 + kpart;                              // this warp's next unit
     for (int p = u0; p < u1; p += kPU) {
         const int pe = p + kPU < u1 ? p + kPU : u1;
-        __syncthreads();                                      // the last x is used up
-        stage_x(a, xs, kXStride, row0, rows, p * kUnitK, (pe - p) * kUnitK);
+        StageX<T, G, NB, kPU> sx;
+        sx.load(a, row0, rows, p * kUnitK, (pe - p) * kUnitK);
+        const bool fast = !__syncthreads_or(sx.beyond());     // and the last x is used up
+        sx.store(xs, kXStride, starts, rows, fast);
         __syncthreads();
         for (; u < pe; u += a.kparts) {
             cp_wait<kStages - 2>();
@@ -311,63 +424,9 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
             const uint32_t st = ring + get * kStageBytes;
             get = get + 1 == kStages ? 0 : get + 1;
             if (!on) continue;
-            const uint32_t xu = xaddr + (u - p) * (kUnitK * 2);
-            float part[2][NB][4];
-            auto clear = [&]() {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) part[t][nb][i] = 0.f;
-            };
-            // the group's sums times its scales: features g, g + 8, g + 16, g + 24
-            auto flush = [&](int group) {
-                uint32_t lo, hi;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(st + kUnitBytes + group * 64 + g * 8));
-                const float s[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
-                                    __uint_as_float(hi & 0xffff0000u)};
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[t][nb][i] = fmaf(s[2 * t + (i >> 1)], part[t][nb][i], acc[t][nb][i]);
-            };
-            clear();
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                uint4 w[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) w[t] = lds128(st + (ch * 2 + t) * 512 + lane * 16);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {        // two steps of 16 inputs
-                    uint4 xv[NB];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) xv[nb] = lds128(xu + nb * (8 * kXStride) + ch * 128 + half * 16);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const uint32_t v = half ? (j ? w[t].w : w[t].z) : (j ? w[t].y : w[t].x);
-                            uint32_t av[4];
-                            deq.operands(v, av);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-                                Deq<T>::mma(part[t][nb], av, j ? xv[nb].z : xv[nb].x, j ? xv[nb].w : xv[nb].y);
-                        }
-                    if (G == 32) {
-                        flush(ch * 2 + half);
-                        if (ch * 2 + half < 3) clear();
-                    }
-                }
-                if (G == 64) {
-                    flush(ch);
-                    if (ch == 0) clear();
-                }
-            }
-            if (G == 128) flush(0);
+            const uint32_t xu = xaddr + (u - p) * (kUnitK * 2), sa = saddr + (u - p) * (kGroups * 8 * NB * 4);
+            if (fast) w4_unit<T, G, NB, true>(acc, st, xu, 8 * kXStride, sa);
+            else w4_unit<T, G, NB, false>(acc, st, xu, 8 * kXStride, sa);
         }
     }
 
@@ -400,8 +459,6 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
                 for (int q = 0; q < (GATED ? 2 : 1); ++q)
                     v[q] += src[(kp * fw + q * fwt + f / kBlockF) * kWarpRed + n * kRedStride + f % kBlockF];
         }
-        v[0] *= Deq<T>::kScale;
-        v[1] *= Deq<T>::kScale;
         const float y = GATED ? gelu_of(v[0]) * v[1] : v[0];
         const size_t at = static_cast<size_t>(row0 + n) * a.N + feature;
         if (a.out_f32) static_cast<float *>(a.y)[at] = y;
@@ -412,64 +469,104 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     else __syncthreads();
 }
 
-template <class T, int G, bool GATED>
+// MAXNB: the most slabs of 8 rows an expert can have (1, 2, or 4: any number); fewer leave the registers to the others.
+template <class T, int G, bool GATED, int MAXNB>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
 {
     extern __shared__ __align__(16) char w4_smem[];
+    griddep_launch_dependents();   // a product that follows gets ready meanwhile; it waits for this one's end by itself
     const int e = blockIdx.y;
     int r0 = 0, r1 = a.R;
     if (a.offsets) {
+        griddep_wait();            // without row ranges the first weights are on their way before this (w4_pass)
         r0 = max(__ldg(a.offsets + e), 0);
         r1 = min(__ldg(a.offsets + e + 1), a.R);
     }
     // all blocks of a cluster have the same expert: they leave, and pass, together
     for (; r0 < r1; r0 += 32) {
         const int rows = min(r1 - r0, 32);
-        if (rows <= 8) w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
-        else if (rows <= 16) w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
-        else w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
+        if (MAXNB == 1 || rows <= 8) {
+            w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
+            continue;
+        }
+        if constexpr (MAXNB > 1) {
+            if (MAXNB == 2 || rows <= 16) {
+                w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
+                continue;
+            }
+        }
+        if constexpr (MAXNB > 2) w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
     }
 }
 
 constexpr int smem_bytes(int G)
 {
-    return kWarps * kStages * (kUnitBytes + kUnitK / G * 64) + 8 * (kXUnits * kUnitK * 2 + 16) + 4 * 8 * 16;
+    // the ring, x with its rows' padding (most with four slabs of 8 rows), the starting values
+    return kWarps * kStages * (kUnitBytes + kUnitK / G * 64) + 8 * (kXUnits * kUnitK * 2) + 4 * 8 * 16 +
+           kXUnits * (kUnitK / G) * 8 * 4;
+}
+
+// How a call is cut: kparts warps share a feature block's inputs, `splits` blocks of a cluster the input range.
+// The estimate counts microseconds as measured here: a warp's step (one unit, eight warps a block) takes 0.53 in a block
+// that has an SM to itself and 0.9 where two share one; a block's start and end 3, plus 0.17 for every row of
+// every phase of staged x, plus 2 for a cluster.  slots: blocks that run together, fewer where clusters do not
+// fill the groups of SMs.  Examples (us, chosen and next best of the other kind): 2 experts of 32768 x 6144, one
+// row each, 5 splits 54 against 60 with two warps an input range and 4 splits, 138 with neither;
+// 64 experts of 2048 x 1408, 2 kparts 29.5, 1 kpart 31.6, 2 splits 35.
+struct W4Cut {
+    int splits, kparts;
+};
+
+W4Cut cut_of(int blocks, int units, int busy, int rows, bool gated)
+{
+    static const int slots[9] = {0, 296, 296, 279, 284, 280, 270, 259, 264};
+    const int slabs = rows <= 8 ? 1 : rows <= 16 ? 2 : 4, phase = kXUnits / slabs;
+    W4Cut best{1, 1};
+    double least = 0;
+    for (int kp = 1; kp <= (gated ? 4 : 8); kp *= 2) {
+        const int fwt = kWarps / kp / (gated ? 2 : 1);
+        const long tiles = static_cast<long>((blocks + fwt - 1) / fwt) * busy;
+        for (int sp = 1; sp <= 8 && sp <= units; ++sp) {
+            const long ctas = tiles * sp, full = ctas / slots[sp], rest = ctas - full * slots[sp];
+            const int share = (units + sp - 1) / sp, walk = (share + kp - 1) / kp, phases = (share + phase - 1) / phase;
+            const double ends = 3 + 0.17 * (rows < 32 ? rows : 32) * phases + (sp > 1 ? 2 : 0);
+            double cost = full * (0.9 * walk + ends);
+            if (rest) cost += (rest <= kSms && sp <= 2 ? 0.53 : 0.9) * walk + ends;
+            if (least == 0 || cost < least) {
+                least = cost;
+                best = W4Cut{sp, kp};
+            }
+        }
+    }
+    return best;
+}
+
+template <class T, int G, bool GATED, int MAXNB>
+cudaError_t launch_w4_rows(const W4Args &a, dim3 grid, cudaStream_t s)
+{
+    constexpr int smem = smem_bytes(G);
+    static_assert(smem >= kWarps * 4 * 8 * kRedStride * 4, "the partial sums take the ring's place");
+    const cudaError_t e =
+        cudaFuncSetAttribute(w4_kernel<T, G, GATED, MAXNB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
+    }
+    return op_launch(w4_kernel<T, G, GATED, MAXNB>, grid, dim3(kWarps * 32), smem, s, true, a.splits, a);
 }
 
 template <class T, int G, bool GATED>
 cudaError_t launch_w4(W4Args a, cudaStream_t s)
 {
-    constexpr int smem = smem_bytes(G);
-    static_assert(smem >= kWarps * 4 * 8 * kRedStride * 4, "the partial sums take the ring's place");
-    const cudaError_t e =
-        cudaFuncSetAttribute(w4_kernel<T, G, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return e;
-    }
-    // Warps on the inputs and blocks on the inputs: the fewest rounds of the SMs' two blocks, counted
-    // in units a warp walks, with half a unit for each round's start and end.  At most as many experts
-    // have work as there are rows.
+    // at most as many experts have work as there are rows
     const int busy = a.offsets && a.R < a.E ? a.R : a.E;
-    double best = 0;
-    for (int kp = 1; kp <= (GATED ? 4 : 8); kp *= 2) {
-        const int fwt = kWarps / kp / (GATED ? 2 : 1);
-        const long tiles = static_cast<long>((a.blocks + fwt - 1) / fwt) * busy;
-        for (int sp = 1; sp <= 8; ++sp) {
-            if (sp > 1 && sp * kp > a.units) break;
-            const long rounds = (tiles * sp + 2 * kSms - 1) / (2 * kSms);
-            const int walk = ((a.units + sp - 1) / sp + kp - 1) / kp;
-            const double cost = rounds * (walk + 4.0) + 0.1 * sp;
-            if (best == 0 || cost < best) {
-                best = cost;
-                a.splits = sp;
-                a.kparts = kp;
-            }
-        }
-    }
+    const W4Cut cut = cut_of(a.blocks, a.units, busy, (a.R + busy - 1) / busy, GATED);
+    a.splits = cut.splits;
+    a.kparts = cut.kparts;
     const int fwt = kWarps / a.kparts / (GATED ? 2 : 1);
     const dim3 grid(static_cast<unsigned>((a.blocks + fwt - 1) / fwt * a.splits), a.E);
-    return op_launch(w4_kernel<T, G, GATED>, grid, dim3(kWarps * 32), smem, s, false, a.splits, a);
+    if (a.R <= 8) return launch_w4_rows<T, G, GATED, 1>(a, grid, s);
+    return a.R <= 16 ? launch_w4_rows<T, G, GATED, 2>(a, grid, s) : launch_w4_rows<T, G, GATED, 4>(a, grid, s);
 }
 
 template <class T>

@@ -124,13 +124,14 @@ def norm_grad(x, gain, stats, dy, layer, dtype):
 def w4(x, offsets, packs, group, dtype):
     """x [R, K], packs = [(q [E, K, N], s [E, groups, N])] (two: gated) -> y (nan in rows of no expert), bound.
 
-    A multiply step adds 16 exact products and the running sum, each cut at the place of the largest: at most
-    17 * 2 U of the group's sizes a step; then one rounding a group, and at most 40 joins."""
+    A group's sum may be taken as that of x (q + 8) and -8 times that of x, so its sizes are |x| (q + 16) s.  A multiply
+    step adds 16 exact products and the running sum, each cut at the place of the largest: at most 17 * 2 U of those
+    sizes a step; then G / 8 + 8 additions for the sum of x, one rounding a group, and at most 40 joins."""
     R, K = x.shape
     N = packs[0][0].shape[2]
     y = torch.full((R, N), math.nan, dtype=F8)
     tol = torch.zeros_like(y)
-    count = 34 * group / 16 + 2 * math.ceil(K / group) + 40
+    count = 34 * group / 16 + group / 8 + 8 + 2 * math.ceil(K / group) + 40
     for e in range(len(offsets) - 1):
         r0, r1 = max(int(offsets[e]), 0), min(int(offsets[e + 1]), R)
         if r0 >= r1:
@@ -138,9 +139,9 @@ def w4(x, offsets, packs, group, dtype):
         xe = x[r0:r1].to(F8)
         v, dv = [], []
         for q, s in packs:
-            w = q[e].to(F8) * s[e].to(F8).repeat_interleave(group, 0)[:K]
-            v.append(xe @ w)
-            dv.append(count * U * (xe.abs() @ w.abs()))
+            se = s[e].to(F8).repeat_interleave(group, 0)[:K]
+            v.append(xe @ (q[e].to(F8) * se))
+            dv.append(count * U * (xe.abs() @ ((q[e].to(F8) + 16) * se.abs())))
         if len(packs) == 1:
             y[r0:r1], tol[r0:r1] = v[0], dv[0]
             continue

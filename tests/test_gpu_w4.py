@@ -181,3 +181,57 @@ def test_weights_beyond_2_gib(m):
     m.check(m.moe_w4_matvec(m.MOE_BF16, m.MOE_F32, E, K, N, group, 3, x, offsets, p, None, y))
     want = (x.double() @ q[0].double()) * 2.0 ** -6    # whole numbers below 2^24: exact in fp32
     assert torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 26, 2.0 ** 27, 2.0 ** 100, 2.0 ** -60, 2.0 ** -90])
+@pytest.mark.parametrize("rows", [3, 20])
+def test_bf16_inputs_of_any_size(m, scale, rows):
+    """Inputs on both sides of the size from which on a phase takes the exact form, alone and mixed with ordinary ones
+    in other places of the same rows (phases of 2048 inputs and fewer), and tiny ones."""
+    K = 5000
+    pk = weights(1, K, 96, 128, 21)
+    x = torch.randn((rows, K), generator=torch.Generator().manual_seed(5))
+    x[:, K // 3:K // 2] *= scale
+    x[rows // 2] *= scale if scale < 2.0 ** 50 else 1
+    x = x.to(torch.bfloat16)
+    ref, tol = ops64.w4(x, [0, rows], [pk], 128, torch.float32)
+    check_rows(run(m, 0, 2, x, None, [pk], 128, (1, K, 96)), ref, tol)
+
+
+def test_subnormal_inputs(m):
+    """Subnormal fp16 inputs count like any others."""
+    pk = weights(1, 256, 64, 32, 2)
+    x = (torch.randn((4, 256), generator=torch.Generator().manual_seed(1)) * 2.0 ** -18).to(torch.float16)
+    ref, tol = ops64.w4(x, [0, 4], [pk], 32, torch.float32)
+    check_rows(run(m, 1, 2, x, None, [pk], 32, (1, 256, 64)), ref, tol)
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+def test_weights_of_zero(m, dt):
+    """Weights that are all 0, next to others: what is left of the inputs' sum is a rounding of it."""
+    q, s = weights(1, 640, 64, 64, 2)
+    q[:, :, ::2] = 0
+    x = torch.randn((5, 640), generator=torch.Generator().manual_seed(1)).to(DT[dt])
+    ref, tol = ops64.w4(x, [0, 5], [(q, s)], 64, torch.float32)
+    assert (ref[:, ::2] == 0).all()
+    check_rows(run(m, dt, 2, x, None, [(q, s)], 64, (1, 640, 64)), ref, tol)
+
+
+def test_a_product_right_behind_another(m):
+    """Products in a row on one stream, each reading what the one before wrote (a launch may begin before its
+    predecessor has ended), give the same bits as with a wait between them."""
+    d, f = 512, 2048
+    up, down = pack(m, *weights(1, d, f, 64, 1), 64), pack(m, *weights(1, f, d, 64, 2), 64)
+    x0 = torch.randn((6, d), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda() / 8
+
+    def chain(wait):
+        x, mid = x0.clone(), torch.empty((6, f), dtype=torch.bfloat16, device="cuda")
+        for _ in range(8):
+            for a, b, w, K, N in ((x, mid, up, d, f), (mid, x, down, f, d)):
+                m.check(m.moe_w4_matvec(0, 0, 1, K, N, 64, 6, a, None, w, None, b))
+                if wait:
+                    torch.cuda.synchronize()
+        return x
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
