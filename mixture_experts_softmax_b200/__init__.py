@@ -309,27 +309,36 @@ def _torch_side():
     import torch
     kinds = {MOE_BF16: torch.bfloat16, MOE_F16: torch.float16, MOE_F32: torch.float32,
              "i32": torch.int32, "i8": torch.int8, "u8": torch.uint8}
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _torch = (kinds, torch.cuda.current_device, raw)
+    if not torch.cuda.is_available():
+        _torch = (kinds, lambda: -2, None)
+        return _torch
+    torch.cuda.current_device()   # torch's own set-up, which the short ways below leave out
+    # the short ways, where torch has them: small calls last a few microseconds
+    _torch = (kinds, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+              getattr(torch._C, "_cuda_getCurrentRawStream", None))
     return _torch
 
 
-def _op_stream(stream):
-    """stream, or the current one of the current device (the short way: small calls last a few microseconds)."""
+def _device() -> int:
+    """The current CUDA device (-2 without one: no tensor is on it)."""
+    return (_torch or _torch_side())[1]()
+
+
+def _op_stream(stream, device):
+    """stream, or the current one of the device."""
     if stream is not None:
         return _stream(stream)
-    _, device, raw = _torch or _torch_side()
-    return raw(device()) if raw else _stream(None)
+    raw = _torch[2]
+    return raw(device) if raw else _stream(None)
 
 
-def _arg(t, name, code, numel):
+def _arg(t, name, code, numel, device):
     """Address of one operand.  code: its element type; numel: the elements that the call may touch."""
     if t is None or isinstance(t, int):
         return t
-    kinds, device, _ = _torch or _torch_side()
-    want = kinds.get(code)
+    want = _torch[0].get(code)
     try:
-        if t.dtype is want and t.is_cuda and t.is_contiguous() and t.numel() >= numel and t.get_device() == device():
+        if t.dtype is want and t.get_device() == device and t.is_contiguous() and t.numel() >= numel:
             return t.data_ptr()
     except AttributeError:
         raise TypeError(f"{name}: cannot pass {type(t).__name__} as a pointer") from None
@@ -339,46 +348,51 @@ def _arg(t, name, code, numel):
         raise ValueError(f"{name}: {t.dtype}, needs {want}")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, needs {numel}")
-    if t.get_device() != device():
+    if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, which is not the current device")
     return t.data_ptr()   # an unknown type code: the C side refuses it
 
 
 def moe_sort_rows(dtype, T, k, E, d, x, idx, offsets, perm, slot, rows, stream=None) -> int:
+    dev = _device()
     n = T * k
-    return _lib.moe_sort_rows(dtype, T, k, E, d, _arg(x, "x", dtype, T * d), _arg(idx, "idx", "i32", n),
-                              _arg(offsets, "offsets", "i32", E + 1), _arg(perm, "perm", "i32", n),
-                              _arg(slot, "slot", "i32", n), _arg(rows, "rows", dtype, n * d), _op_stream(stream))
+    return _lib.moe_sort_rows(dtype, T, k, E, d, _arg(x, "x", dtype, T * d, dev), _arg(idx, "idx", "i32", n, dev),
+                              _arg(offsets, "offsets", "i32", E + 1, dev), _arg(perm, "perm", "i32", n, dev),
+                              _arg(slot, "slot", "i32", n, dev), _arg(rows, "rows", dtype, n * d, dev), _op_stream(stream, dev))
 
 
 def moe_unsort_rows(rows_dtype, dtype, T, k, d, rows, slot, gate, out, stream=None) -> int:
     """Also the gradient of moe_sort_rows' x: rows = the rows' gradient, gate = None."""
+    dev = _device()
     n = T * k
-    return _lib.moe_unsort_rows(rows_dtype, dtype, T, k, d, _arg(rows, "rows", rows_dtype, n * d),
-                                _arg(slot, "slot", "i32", n), _arg(gate, "gate", MOE_F32, n),
-                                _arg(out, "out", dtype, T * d), _op_stream(stream))
+    return _lib.moe_unsort_rows(rows_dtype, dtype, T, k, d, _arg(rows, "rows", rows_dtype, n * d, dev),
+                                _arg(slot, "slot", "i32", n, dev), _arg(gate, "gate", MOE_F32, n, dev),
+                                _arg(out, "out", dtype, T * d, dev), _op_stream(stream, dev))
 
 
 def moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, dout, rows, slot, gate, drows, dgate, stream=None) -> int:
+    dev = _device()
     n = T * k
-    return _lib.moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, _arg(dout, "dout", dtype, T * d),
-                                         _arg(rows, "rows", rows_dtype, n * d), _arg(slot, "slot", "i32", n),
-                                         _arg(gate, "gate", MOE_F32, n), _arg(drows, "drows", rows_dtype, n * d),
-                                         _arg(dgate, "dgate", MOE_F32, n), _op_stream(stream))
+    return _lib.moe_unsort_rows_backward(rows_dtype, dtype, T, k, d, _arg(dout, "dout", dtype, T * d, dev),
+                                         _arg(rows, "rows", rows_dtype, n * d, dev), _arg(slot, "slot", "i32", n, dev),
+                                         _arg(gate, "gate", MOE_F32, n, dev), _arg(drows, "drows", rows_dtype, n * d, dev),
+                                         _arg(dgate, "dgate", MOE_F32, n, dev), _op_stream(stream, dev))
 
 
 def moe_norm_forward(kind, dtype, T, d, x, gain, bias, eps, y, stats=None, stream=None) -> int:
-    return _lib.moe_norm_forward(kind, dtype, T, d, _arg(x, "x", dtype, T * d), _arg(gain, "gain", dtype, d),
-                                 _arg(bias, "bias", dtype, d), eps, _arg(y, "y", dtype, T * d),
-                                 _arg(stats, "stats", MOE_F32, 2 * T), _op_stream(stream))
+    dev = _device()
+    return _lib.moe_norm_forward(kind, dtype, T, d, _arg(x, "x", dtype, T * d, dev), _arg(gain, "gain", dtype, d, dev),
+                                 _arg(bias, "bias", dtype, d, dev), eps, _arg(y, "y", dtype, T * d, dev),
+                                 _arg(stats, "stats", MOE_F32, 2 * T, dev), _op_stream(stream, dev))
 
 
 def moe_norm_backward(kind, dtype, T, d, x, gain, stats, dy, dx, dgain, dbias, workspace, stream=None) -> int:
-    return _lib.moe_norm_backward(kind, dtype, T, d, _arg(x, "x", dtype, T * d), _arg(gain, "gain", dtype, d),
-                                  _arg(stats, "stats", MOE_F32, 2 * T), _arg(dy, "dy", dtype, T * d),
-                                  _arg(dx, "dx", dtype, T * d), _arg(dgain, "dgain", MOE_F32, d),
-                                  _arg(dbias, "dbias", MOE_F32, d),
-                                  _arg(workspace, "workspace", "u8", moe_norm_workspace(T, d)), _op_stream(stream))
+    dev = _device()
+    return _lib.moe_norm_backward(kind, dtype, T, d, _arg(x, "x", dtype, T * d, dev), _arg(gain, "gain", dtype, d, dev),
+                                  _arg(stats, "stats", MOE_F32, 2 * T, dev), _arg(dy, "dy", dtype, T * d, dev),
+                                  _arg(dx, "dx", dtype, T * d, dev), _arg(dgain, "dgain", MOE_F32, d, dev),
+                                  _arg(dbias, "dbias", MOE_F32, d, dev),
+                                  _arg(workspace, "workspace", "u8", moe_norm_workspace(T, d), dev), _op_stream(stream, dev))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -395,16 +409,19 @@ def moe_w4_packed_bytes(E, K, N, group) -> int:
 
 def moe_w4_pack(E, K, N, group, q, scales, packed, stream=None) -> int:
     """q int8 [E, K, N] in [-8, 7], scales bf16 [E, ceil(K / group), N] -> packed uint8."""
-    return _lib.moe_w4_pack(E, K, N, group, _arg(q, "q", "i8", E * K * N),
-                            _arg(scales, "scales", MOE_BF16, E * -(-K // max(group, 1)) * N),
-                            _arg(packed, "packed", "u8", moe_w4_packed_bytes(E, K, N, group)), _op_stream(stream))
+    dev = _device()
+    return _lib.moe_w4_pack(E, K, N, group, _arg(q, "q", "i8", E * K * N, dev),
+                            _arg(scales, "scales", MOE_BF16, E * -(-K // max(group, 1)) * N, dev),
+                            _arg(packed, "packed", "u8", moe_w4_packed_bytes(E, K, N, group), dev), _op_stream(stream, dev))
 
 
 def moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, x, offsets, packed, packed_v, y, stream=None) -> int:
+    dev = _device()
     nbytes = moe_w4_packed_bytes(E, K, N, group)
-    return _lib.moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, _arg(x, "x", dtype, R * K),
-                              _arg(offsets, "offsets", "i32", E + 1), _arg(packed, "packed", "u8", nbytes),
-                              _arg(packed_v, "packed_v", "u8", nbytes), _arg(y, "y", out_dtype, R * N), _op_stream(stream))
+    return _lib.moe_w4_matvec(dtype, out_dtype, E, K, N, group, R, _arg(x, "x", dtype, R * K, dev),
+                              _arg(offsets, "offsets", "i32", E + 1, dev), _arg(packed, "packed", "u8", nbytes, dev),
+                              _arg(packed_v, "packed_v", "u8", nbytes, dev), _arg(y, "y", out_dtype, R * N, dev),
+                              _op_stream(stream, dev))
 
 
 def moe_plan(h, T: int):
