@@ -283,9 +283,17 @@ struct Rows {
     __device__ __forceinline__ void columns(char *dst, const void *src, float fill) const
     {
         T *out = reinterpret_cast<T *>(dst);
-        for (int i = threadIdx.x; i < at.nv * W; i += blockDim.x) {
-            const int c = i - at.shift;
-            out[i] = src && c >= 0 && c < at.d ? static_cast<const T *>(src)[c] : from_f32<T>(fill);
+        const int n = at.nv * W, step = blockDim.x;
+        for (int i0 = threadIdx.x; i0 < n; i0 += 8 * step) {
+            T v[8];   // in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = i0 + k * step - at.shift;
+                v[k] = src && c >= 0 && c < at.d ? __ldg(static_cast<const T *>(src) + c) : from_f32<T>(fill);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + k * step < n) out[i0 + k * step] = v[k];
         }
     }
 };
