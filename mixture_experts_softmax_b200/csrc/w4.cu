@@ -469,33 +469,64 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     else __syncthreads();
 }
 
+// the n-th expert that has rows, and its rows; the whole warp asks together
+__device__ __forceinline__ bool busy_expert(const W4Args &a, int n, int &e, int &r0, int &r1)
+{
+    if (!a.offsets) {
+        e = 0;
+        r0 = 0;
+        r1 = a.R;
+        return n == 0;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int mine = e0 + lane;
+        int lo = 0, hi = 0;
+        if (mine < a.E) {
+            lo = max(__ldg(a.offsets + mine), 0);
+            hi = min(__ldg(a.offsets + mine + 1), a.R);
+        }
+        unsigned m = __ballot_sync(0xffffffffu, lo < hi);
+        const int here = __popc(m);
+        if (n < here) {
+            for (; n > 0; --n) m &= m - 1;
+            const int at = __ffs(m) - 1;
+            e = e0 + at;
+            r0 = __shfl_sync(0xffffffffu, lo, at);
+            r1 = __shfl_sync(0xffffffffu, hi, at);
+            return true;
+        }
+        n -= here;
+    }
+    return false;
+}
+
 // MAXNB: the most slabs of 8 rows an expert can have (1, 2, or 4: any number); fewer leave the registers to the others.
 template <class T, int G, bool GATED, int MAXNB>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
 {
     extern __shared__ __align__(16) char w4_smem[];
     griddep_launch_dependents();   // a product that follows gets ready meanwhile; it waits for this one's end by itself
-    const int e = blockIdx.y;
-    int r0 = 0, r1 = a.R;
-    if (a.offsets) {
-        griddep_wait();            // without row ranges the first weights are on their way before this (w4_pass)
-        r0 = max(__ldg(a.offsets + e), 0);
-        r1 = min(__ldg(a.offsets + e + 1), a.R);
-    }
-    // all blocks of a cluster have the same expert: they leave, and pass, together
-    for (; r0 < r1; r0 += 32) {
-        const int rows = min(r1 - r0, 32);
-        if (MAXNB == 1 || rows <= 8) {
-            w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
-            continue;
-        }
-        if constexpr (MAXNB > 1) {
-            if (MAXNB == 2 || rows <= 16) {
-                w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
+    if (a.offsets) griddep_wait();   // without row ranges the first weights are on their way before this (w4_pass)
+    // All blocks of a cluster have the same expert: they leave, and pass, together.  The grid has a row of blocks for
+    // every expert that can have work, not for every expert.
+    for (int i = blockIdx.y;; i += gridDim.y) {
+        int e, r0, r1;
+        if (!busy_expert(a, i, e, r0, r1)) return;
+        for (; r0 < r1; r0 += 32) {
+            const int rows = min(r1 - r0, 32);
+            if (MAXNB == 1 || rows <= 8) {
+                w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
                 continue;
             }
+            if constexpr (MAXNB > 1) {
+                if (MAXNB == 2 || rows <= 16) {
+                    w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
+                    continue;
+                }
+            }
+            if constexpr (MAXNB > 2) w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
         }
-        if constexpr (MAXNB > 2) w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
     }
 }
 
@@ -564,7 +595,7 @@ cudaError_t launch_w4(W4Args a, cudaStream_t s)
     a.splits = cut.splits;
     a.kparts = cut.kparts;
     const int fwt = kWarps / a.kparts / (GATED ? 2 : 1);
-    const dim3 grid(static_cast<unsigned>((a.blocks + fwt - 1) / fwt * a.splits), a.E);
+    const dim3 grid(static_cast<unsigned>((a.blocks + fwt - 1) / fwt * a.splits), busy);
     if (a.R <= 8) return launch_w4_rows<T, G, GATED, 1>(a, grid, s);
     return a.R <= 16 ? launch_w4_rows<T, G, GATED, 2>(a, grid, s) : launch_w4_rows<T, G, GATED, 4>(a, grid, s);
 }

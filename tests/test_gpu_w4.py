@@ -235,3 +235,26 @@ def test_a_product_right_behind_another(m):
     want = chain(True)
     for _ in range(5):
         assert torch.equal(chain(False), want)
+
+
+def test_few_rows_of_many_experts(m):
+    """Rows at the first, some middle and the last of many experts; fewer rows than experts."""
+    E, K, N = 70, 200, 96
+    pk = weights(E, K, N, 64, 3)
+    for at in ([0, 31, 69], [3, 32, 33], [69, 69, 69]):
+        x = torch.randn((3, K), generator=torch.Generator().manual_seed(at[0])).to(torch.bfloat16)
+        offsets = [sum(e < i for e in at) for i in range(E + 1)]
+        ref, tol = ops64.w4(x, offsets, [pk], 64, torch.float32)
+        assert not ref.isnan().any()
+        check_rows(run(m, 0, 2, x, offsets, [pk], 64, (E, K, N)), ref, tol)
+
+
+def test_ranges_that_overlap(m):
+    """More ranges than rows: every row that lies in a range gets the product of one it lies in."""
+    pk = weights(5, 96, 32, 32, 4)
+    x = torch.randn((2, 96), generator=torch.Generator().manual_seed(0)).to(torch.float16)
+    got = run(m, 1, 2, x, [0, 1, 0, 1, 0, 2], [pk], 32, (5, 96, 32))
+    one, tol = ops64.w4(x, [0, 0, 0, 0, 0, 2], [pk], 32, torch.float32)
+    ops64.assert_close(got[1:], one[1:], tol[1:])
+    first = [ops64.w4(x, [0] * (e + 1) + [1] * (5 - e), [pk], 32, torch.float32) for e in (0, 2, 4)]
+    assert any(((got[0].double() - r[0]).abs() <= t[0]).all() for r, t in first)
