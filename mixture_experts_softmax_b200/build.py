@@ -12,6 +12,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -45,10 +47,20 @@ def stale() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not stale():
         return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-o", LIB + ".tmp", *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    tool = nvcc()
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    # every source by itself, side by side, then one link
+    with tempfile.TemporaryDirectory() as objects:
+        outs = [os.path.join(objects, os.path.basename(src) + ".o") for src in SOURCES]
+        compile_flags = [f for f in NVCC_FLAGS if f not in ("-shared", "-cudart", "static")]
+        with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: run([tool, *compile_flags, *extra, "-c", "-o", so[1], so[0]]), zip(SOURCES, outs)))
+        run([tool, *NVCC_FLAGS, "-o", LIB + ".tmp", *outs])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 
