@@ -36,11 +36,11 @@ inline bool dtype_known(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F1
 // MOE_OK if the current device can run the library's sm_100a code
 int op_device();
 
-// launch with the attributes the operators use; pdl: the kernel may be scheduled while its
-// predecessor on the stream ends and waits for it itself (griddep_wait)
+// Launch with the attributes the operators use.  early: the kernel may be scheduled while its predecessor on the stream
+// ends; it begins with op_begin(), which waits for that end.
 template <class... P, class... A>
-cudaError_t op_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool pdl, int cluster,
-                      A... args)
+cudaError_t op_launch_when(bool early, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                           A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -49,7 +49,7 @@ cudaError_t op_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, 
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (pdl) {
+    if (early) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[n++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -66,7 +66,22 @@ cudaError_t op_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, 
     return e;
 }
 
+template <class... P, class... A>
+cudaError_t op_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster, A... args)
+{
+    return op_launch_when(true, kernel, grid, block, smem, s, cluster, args...);
+}
+
 // ---- device side ---------------------------------------------------------------
+
+// The first thing every thread does: wait until all earlier work on the stream has ended and its writes are visible,
+// then let the next launch get its blocks ready behind this one's.  In this order, so that a launch never
+// begins before the work two launches back has ended.  Saves the launch gap of 2 to 3 us between kernels.
+__device__ __forceinline__ void op_begin()
+{
+    griddep_wait();
+    griddep_launch_dependents();
+}
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) sort_plan_kernel(SortArgs a, 
     __shared__ int tot[kMaxSortExperts], all[kMaxSortExperts], first[kMaxSortExperts], base[kMaxSortExperts + 1];
     cg::cluster_group cl = cg::this_cluster();
     const int C = cl.num_blocks(), rank = cl.block_rank(), warp = threadIdx.x >> 5;
-    griddep_launch_dependents();   // the copy of the rows waits for this kernel's end where it has to
+    op_begin();
 
     const int per = ((a.n + C * kPlanWarps - 1) / (C * kPlanWarps) + 31) / 32 * 32;
     // long: the last warps' segments may begin behind the end of the range of an int
@@ -239,7 +239,7 @@ __device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long 
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
         if (v0 + u * lanes < c.vpr) v[u] = __ldg(src + v0 + u * lanes);
-    if (wait) griddep_wait();   // x was there before the call; the slots are the previous kernel's
+    if (wait) op_begin();   // x is older than the order's launch, which had waited before this one could begin
     if (!on) return;
     for (int j0 = 0; j0 < k; j0 += kUnroll) {
         int row[kUnroll];
@@ -273,6 +273,7 @@ constexpr int kSmallRoutes = 1024;
 template <class V>
 __global__ void __launch_bounds__(kSmallWarps * 32) sort_small_kernel(SortArgs a, CopyArgs c)
 {
+    op_begin();
     __shared__ int cnt[kSmallStride * kMaxSortExperts];
     __shared__ int tot[kMaxSortExperts], base[kMaxSortExperts + 1];
     __shared__ int slots[kSmallRoutes];
@@ -320,12 +321,12 @@ cudaError_t launch_sort(const SortArgs &a, const void *x, void *rows, size_t row
     c.units = static_cast<long>(a.T) * c.upr;
     const unsigned grid = static_cast<unsigned>(((c.units << c.lg) + 255) / 256);
     if (a.n <= kSmallRoutes)
-        return op_launch(sort_small_kernel<V>, dim3(x ? grid : 1), dim3(kSmallWarps * 32), 0, s, false, 1, a, c);
+        return op_launch(sort_small_kernel<V>, dim3(x ? grid : 1), dim3(kSmallWarps * 32), 0, s, 1, a, c);
     // one step a warp as far as the cluster goes
     const int cluster = a.n <= 2048 ? 2 : a.n <= 4096 ? 4 : 8;
-    cudaError_t e = op_launch(sort_plan_kernel, dim3(cluster), dim3(kPlanWarps * 32), 0, s, false, cluster, a, x ? 0 : 1);
+    cudaError_t e = op_launch(sort_plan_kernel, dim3(cluster), dim3(kPlanWarps * 32), 0, s, cluster, a, x ? 0 : 1);
     if (e != cudaSuccess || !x) return e;
-    return op_launch(sort_copy_kernel<V>, dim3(grid), dim3(256), 0, s, true, 1, c, static_cast<const int *>(a.slot), a.k,
+    return op_launch(sort_copy_kernel<V>, dim3(grid), dim3(256), 0, s, 1, c, static_cast<const int *>(a.slot), a.k,
                      a.n, a.perm);
 }
 
@@ -366,6 +367,7 @@ template <class R, int N, int G> constexpr int unsort_steps() { return steps_of(
 template <class R, class O, int N, int G, int NT>
 __global__ void __launch_bounds__(256) unsort_kernel(UnsortArgs a, int threads)
 {
+    op_begin();
     const int nt = NT ? NT : threads;
     constexpr int kSteps = unsort_steps<R, N, G>();
     const int n = a.T * a.k, sub = static_cast<int>(threadIdx.x) / nt, lane = static_cast<int>(threadIdx.x) - sub * nt;
@@ -431,6 +433,7 @@ constexpr int unsort_grad_steps() { return steps_of(N * static_cast<int>(sizeof(
 template <class R, class O, int N, int G, int NT>
 __global__ void __launch_bounds__(256) unsort_grad_kernel(UnsortGradArgs a, int threads)
 {
+    op_begin();
     const int nt = NT ? NT : threads;
     constexpr int kSteps = unsort_grad_steps<R, O, N, G>();
     __shared__ float red[2][8][G];
@@ -528,7 +531,7 @@ cudaError_t launch_unsort_group(const UnsortArgs &a, cudaStream_t s)
     void (*kernel)(UnsortArgs, int);
     if constexpr (N > 2) kernel = unsort_kernel<R, O, N, G, 0>;
     else kernel = sh.nt == 32 ? unsort_kernel<R, O, N, G, 32> : unsort_kernel<R, O, N, G, 256>;
-    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, false, 1, a, sh.nt);
+    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, 1, a, sh.nt);
 }
 
 template <class R, class O, int N>
@@ -544,7 +547,7 @@ cudaError_t launch_unsort_grad_group(const UnsortGradArgs &a, cudaStream_t s)
     void (*kernel)(UnsortGradArgs, int);
     if constexpr (N > 2) kernel = unsort_grad_kernel<R, O, N, G, 0>;
     else kernel = sh.nt == 32 ? unsort_grad_kernel<R, O, N, G, 32> : unsort_grad_kernel<R, O, N, G, 256>;
-    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, false, 1, a, sh.nt);
+    return op_launch(kernel, dim3(sh.grid), dim3(sh.block), 0, s, 1, a, sh.nt);
 }
 
 template <class R, class O, int N>

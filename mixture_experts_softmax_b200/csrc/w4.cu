@@ -58,6 +58,7 @@ W4Shape shape_of(int E, int K, int N, int G)
 // one thread a 32-bit word: lanes of a warp cover the 32 features of 8 inputs
 __global__ void __launch_bounds__(256) w4_pack_kernel(W4Shape s, const int8_t *q, uint32_t *out, int *flag)
 {
+    op_begin();
     const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
     const size_t total = static_cast<size_t>(s.E) * s.blocks * s.units * (kUnitBytes / 4);
     if (i >= total) return;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4Shape s, const int8_t *q
 
 __global__ void __launch_bounds__(256) w4_pack_scales_kernel(W4Shape s, const __nv_bfloat16 *in, __nv_bfloat16 *out)
 {
+    op_begin();
     const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
     const size_t total = static_cast<size_t>(s.E) * s.blocks * s.units * s.per_unit * kBlockF;
     if (i >= total) return;
@@ -407,7 +409,6 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
-    griddep_wait();                                           // x and the rows of y; the weights are nobody's output
 
     int get = 0, u = u0 + kpart;                              // this warp's next unit
     for (int p = u0; p < u1; p += kPU) {
@@ -506,8 +507,7 @@ template <class T, int G, bool GATED, int MAXNB>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
 {
     extern __shared__ __align__(16) char w4_smem[];
-    griddep_launch_dependents();   // a product that follows gets ready meanwhile; it waits for this one's end by itself
-    if (a.offsets) griddep_wait();   // without row ranges the first weights are on their way before this (w4_pass)
+    op_begin();
     // All blocks of a cluster have the same expert: they leave, and pass, together.  The grid has a row of blocks for
     // every expert that can have work, not for every expert.
     for (int i = blockIdx.y;; i += gridDim.y) {
@@ -583,7 +583,7 @@ cudaError_t launch_w4_rows(const W4Args &a, dim3 grid, cudaStream_t s)
         cudaGetLastError();
         return e;
     }
-    return op_launch(w4_kernel<T, G, GATED, MAXNB>, grid, dim3(kWarps * 32), smem, s, true, a.splits, a);
+    return op_launch(w4_kernel<T, G, GATED, MAXNB>, grid, dim3(kWarps * 32), smem, s, a.splits, a);
 }
 
 template <class T, int G, bool GATED>
@@ -643,9 +643,9 @@ extern "C" MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t 
     const size_t words = sh.scales / 4, nscales = (sh.bytes - kTail - sh.scales) / 2;
     int bad = 0;
     if (cudaMemsetAsync(flag, 0, kTail, s) != cudaSuccess ||
-        op_launch(w4_pack_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, false, 1, sh, q,
+        op_launch(w4_pack_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, 1, sh, q,
                   reinterpret_cast<uint32_t *>(out), flag) != cudaSuccess ||
-        op_launch(w4_pack_scales_kernel, dim3(static_cast<unsigned>((nscales + 255) / 256)), dim3(256), 0, s, false, 1, sh,
+        op_launch(w4_pack_scales_kernel, dim3(static_cast<unsigned>((nscales + 255) / 256)), dim3(256), 0, s, 1, sh,
                   static_cast<const __nv_bfloat16 *>(scales), reinterpret_cast<__nv_bfloat16 *>(out + sh.scales)) !=
             cudaSuccess ||
         cudaMemcpyAsync(&bad, flag, sizeof bad, cudaMemcpyDeviceToHost, s) != cudaSuccess ||

@@ -262,3 +262,42 @@ def test_binding_refuses_tensors_it_would_misread(m):
     # a view that begins off a 16-byte boundary is the library's to refuse
     flat = torch.zeros(8 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(8, 64)
     assert m.moe_norm_forward(m.MOE_NORM_RMS, m.MOE_BF16, 8, 64, flat, None, None, 1e-5, y) == m.MOE_EINVAL
+
+
+def test_calls_right_behind_one_another(m):
+    """Launches may be scheduled before their predecessors on the stream have ended: chains of calls that reuse every
+    buffer (rows, workspace, order) with new inputs each turn give the bits of the same chain with waits."""
+    T, k, E, d = 2000, 2, 16, 768
+    g = torch.Generator(device="cuda").manual_seed(4)
+    xs = [torch.randn((T, d), generator=g, device="cuda") for _ in range(4)]
+    idxs = [torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous() for _ in range(4)]
+    gain, gate = torch.randn(d, generator=g, device="cuda"), torch.rand((T, k), generator=g, device="cuda")
+    blk = Block4(m, 8, 256, 512, 64)
+
+    def chain(wait):
+        st, out = Train(m, 1, T, k, E, d), []
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        for turn in range(8):
+            x, idx = xs[turn % 4], idxs[turn * 3 % 4]
+            st.forward(x, gain, None, idx, gate)
+            pause()
+            m.check(m.moe_unsort_rows(m.MOE_F32, m.MOE_F32, T, k, d, st.rows, st.slot, gate, st.out))
+            pause()
+            m.check(m.moe_unsort_rows_backward(m.MOE_F32, m.MOE_F32, T, k, d, st.out, st.rows, st.slot, gate, st.dy, st.dgate))
+            pause()
+            m.check(m.moe_unsort_rows(m.MOE_F32, m.MOE_F32, T, k, d, st.dy, st.slot, None, st.du))
+            pause()
+            m.check(m.moe_norm_backward(1, m.MOE_F32, T, d, x, gain, st.stats, st.du, st.dx, st.dgain, st.dbias, st.ws))
+            pause()
+            out += [t.clone() for t in (st.out, st.dx, st.dgain, st.dbias, st.dgate, st.perm, st.slot)]
+        h = tokens(8, 256, 1).cuda()
+        for _ in range(6):   # the block on its own output, routing and experts in a row
+            blk.h.copy_(h)
+            blk.run()
+            pause()
+            h = blk.out.clone()
+        return out + [h]
+    want = chain(True)
+    for _ in range(3):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
