@@ -15,8 +15,12 @@
 // Rows whose width is no multiple of 16 bytes still move in 16-byte vectors: rows r, r + P, r + 2 P ...
 // (P = 16 bytes over their common divisor with the row) begin at the same place within a vector,
 // so a block that takes rows of one such class has its columns at fixed places.
-// Rows too wide for a block are read again from the caches instead, and their columns' sums
-// taken by a kernel of their own.
+// Rows too wide for a block's registers are read again from the caches instead, with the columns' sums in shared memory
+// or, wider still, taken by a kernel of their own.
+//
+// Measured on a B200: LayerNorm of 16,383 x 2560 fp32 53 us (98% of the copy bandwidth), RMSNorm gradient of 8192 x
+// 6144 bf16 66 us (71%: about 60 us for the rows, at half of all issue slots, and the reduction), LayerNorm
+// gradient of 5003 x 1537 fp16 31 us (23%: each block waits for one row's sums after the other, some 2700 cycles a row).
 #include "ops_common.cuh"
 
 namespace moe {

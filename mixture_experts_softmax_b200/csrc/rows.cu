@@ -7,7 +7,11 @@
 //   gradient  drows[slot[t,j]] = gate[t,j] * dout[t],  dgate[t,j] = <dout[t], rows[slot[t,j]]>
 //
 // All are bound by memory traffic: each row is read once and written once, with 16-byte accesses
-// where the row width allows them, and every sum has a fixed order.
+// where the row width allows them, and every sum has a fixed order.  Measured on a B200 at 8192 tokens, 2
+// picks, 6144 wide: sort bf16 53 us (88% of the copy bandwidth; about 6 us of it are the order, which only few SMs can
+// find), way back of fp32 rows into bf16 75 us and its bf16 gradient 78 us (both at the copy bandwidth).  Rows that
+// are no multiple of 16 bytes move in narrower pieces, and the number of accesses limits them: gradient of
+// 1021 tokens, 6 picks, 2051 fp32 wide 22 us (59%).  Small batches are a launch: 8 tokens 7 us.
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"

@@ -274,3 +274,26 @@ def test_sort_offsets_pass_32_bits(m):
     drows = torch.zeros_like(x)
     m.check(m.moe_unsort_rows_backward(0, 0, T, 1, d, x, None, slot, None, drows, None))
     assert torch.equal(drows, rows)
+
+
+def test_sort_four_million_routes(m):
+    """The most tokens, picks and experts: 262,144 x 16 over 256, a tenth dropped, against a stable sort by key."""
+    T, k, E, d = 262144, 16, 256, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    idx[torch.rand((T, k), generator=g, device="cuda") < 0.1] = -1
+    x = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].expand(T, d).contiguous()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offsets, perm, slot = torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32)
+    rows = torch.full((T * k, d), -1.0, device="cuda")
+    m.check(m.moe_sort_rows(m.MOE_F32, T, k, E, d, x, idx, offsets, perm, slot, rows))
+    flat = idx.flatten().long()
+    key = torch.where(flat >= 0, flat, E)
+    order = key.argsort(stable=True)
+    n = int((flat >= 0).sum())
+    assert torch.equal(perm[:n].long(), order[:n]) and (perm[n:] == -1).all()
+    assert torch.equal(offsets.long(), torch.searchsorted(key[order].contiguous(), torch.arange(E + 1, device="cuda")))
+    want = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    want[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(slot.flatten().long(), want)
+    assert torch.equal(rows[:n, 0].long(), order[:n] // k) and (rows[n:] == -1).all()

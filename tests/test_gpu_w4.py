@@ -258,3 +258,22 @@ def test_ranges_that_overlap(m):
     ops64.assert_close(got[1:], one[1:], tol[1:])
     first = [ops64.w4(x, [0] * (e + 1) + [1] * (5 - e), [pk], 32, torch.float32) for e in (0, 2, 4)]
     assert any(((got[0].double() - r[0]).abs() <= t[0]).all() for r, t in first)
+
+
+def test_most_rows_and_experts(m):
+    """The largest row count, in 32-row passes over one expert; the largest expert count, a row each."""
+    pk = weights(1, 160, 64, 32, 6)
+    x = torch.randn((1024, 160), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    ref, tol = ops64.w4(x, [0, 1024], [pk], 32, torch.bfloat16)
+    check_rows(run(m, 0, 0, x, None, [pk], 32, (1, 160, 64)), ref, tol)
+    pk = weights(1024, 130, 34, 128, 7)
+    ref, tol = ops64.w4(x[:, :130].contiguous(), list(range(1025)), [pk], 128, torch.float32)
+    check_rows(run(m, 0, 2, x[:, :130].contiguous(), list(range(1025)), [pk], 128, (1024, 130, 34)), ref, tol)
+
+
+@pytest.mark.parametrize("K,N", [(131072, 40), (40, 131072)])
+def test_longest_sides(m, K, N):
+    pk = weights(1, K, N, 128, 9)
+    x = torch.randn((2, K), generator=torch.Generator().manual_seed(0)).to(torch.float16)
+    ref, tol = ops64.w4(x, [0, 2], [pk], 128, torch.float32)
+    check_rows(run(m, 1, 2, x, None, [pk], 128, (1, K, N)), ref, tol)
