@@ -35,7 +35,7 @@ namespace {
 constexpr int kBlockF = 32;            // features of a block: one warp's
 constexpr int kUnitK = 128;            // inputs of a unit: one stage
 constexpr int kUnitBytes = kBlockF * kUnitK / 2;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kWarps = 8;
 constexpr int kMaxRows = 1024;
 constexpr int kMaxWExperts = 1024;
