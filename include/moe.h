@@ -558,7 +558,8 @@ MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t *q, const v
  * Made for a few rows an expert: 32 rows share one pass over the weights.  R <= 1024 (else
  * MOE_EUNSUPPORTED).  R == 0 is a no-op.  Sums are fp32.  A group's products are summed with the weights offset by 8 and
  * the offset taken off again, so where all weights are 0 the result is a rounding of the inputs' sum (about 2^-24
- * of it), not an exact 0.  Infinite and nan inputs follow the formula.
+ * of it), not an exact 0.  Infinite and nan inputs follow the formula.  A bf16 input below 2^-100 counts with an
+ * absolute error of up to 2^-112, and the scales are below 2^94.
  */
 MOE_API int moe_w4_matvec(int dtype, int out_dtype, int E, int K, int N, int group, int R, const void *x,
                           const int32_t *offsets, const void *packed, const void *packed_v, void *y, void *stream);

@@ -198,6 +198,20 @@ def test_bf16_inputs_of_any_size(m, scale, rows):
     check_rows(run(m, 0, 2, x, None, [pk], 128, (1, K, 96)), ref, tol)
 
 
+@pytest.mark.parametrize("power", [-98, -104, -110, -118])
+@pytest.mark.parametrize("rows,group", [(3, 32), (5, 128), (20, 64)])
+def test_tiny_bf16_inputs(m, power, rows, group):
+    """Rows of nothing but bf16 inputs around 2^-100 and below: each group of inputs may be off by 2^-112 of its scale
+    beside the usual roundings.  (A product is u x 2^-33 in steps of 2^-149: 9 additions of a group, each off by a step,
+    make 9 * 2^-116.)"""
+    K = 1000
+    q, s = weights(1, K, 96, group, 23)
+    x = (torch.randn((rows, K), generator=torch.Generator().manual_seed(6)) * 2.0 ** power).to(torch.bfloat16)
+    ref, tol = ops64.w4(x, [0, rows], [(q, s)], group, torch.float32)
+    tol = tol + s[0].double().abs().sum(0) * 2.0 ** -112
+    check_rows(run(m, 0, 2, x, None, [(q, s)], group, (1, K, 96)), ref, tol)
+
+
 def test_subnormal_inputs(m):
     """Subnormal fp16 inputs count like any others."""
     pk = weights(1, 256, 64, 32, 2)
