@@ -510,7 +510,8 @@ MOE_API int moe_unsort_rows_backward(int rows_dtype, int dtype, int T, int k, in
  *   stats  fp32  [T, 2]  out: the row's mean (0 for MOE_NORM_RMS) and 1 / sqrt(... + eps), which the
  *                        backward pass takes; or NULL
  * 1 <= d <= 65536, T <= MOE_MAX_TOKENS, eps >= 0.  Statistics are taken in fp32, the variance around
- * the mean.  T == 0 is a no-op.
+ * the mean, and the mean is corrected by the mean of the differences from it: a row of equal values has that
+ * value as its mean at any width.  T == 0 is a no-op.
  */
 MOE_API int moe_norm_forward(int kind, int dtype, int T, int d, const void *x, const void *gain, const void *bias,
                              float eps, void *y, float *stats, void *stream);

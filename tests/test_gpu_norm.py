@@ -196,3 +196,35 @@ def test_offsets_pass_32_bits(m):
     assert torch.equal(y[-16:].cpu(), dx) and (y[:-16] == 0).all()
     _, tols = ops64.norm_grad(tail, gain, wstats, dy, False, DT[0])
     ops64.assert_close(dgain.cpu(), dg.double(), 2 * tols[1])
+
+
+@pytest.mark.parametrize("d", [3, 37, 96, 512, 1022, 1537, 4100, 6144, 8200, 16400, 40001])
+@pytest.mark.parametrize("dt", [0, 1, 2])
+def test_constant_rows_of_any_width(m, d, dt):
+    """Rows of one value, small to large, and of widths whose inverse is no power of two: the mean is that value and y is the
+    bias, both to the bit.  The pivot is off by at most 80 U |x| (the sum's chain and the division), every difference from it is
+    the same exact number e, so q and d m^2 are d e^2 but for 80 + 84 roundings: what is left is the variance's error."""
+    x = torch.tensor([1000.0, -1000.1, 0.3, 30000.7, 1.0, 4096.5]).to(DT[dt])[:, None].expand(6, d).contiguous()
+    gain, bias = torch.full((d,), 2.0).to(DT[dt]), torch.full((d,), 0.5).to(DT[dt])
+    eps = float(torch.tensor(1e-5))
+    y, stats = run_forward(m, 1, dt, x, gain, bias)
+    assert torch.equal(stats[:, 0], x[:, 0].float())
+    assert (y == 0.5).all()
+    left = 164 * ops64.U * (80 * ops64.U * x[:, 0].double()) ** 2
+    want = eps ** -0.5
+    assert ((stats[:, 1].double() - want).abs() <= want * (0.5 * left / eps + 4 * ops64.U)).all()
+
+
+@pytest.mark.parametrize("T,d", [(5, 96), (5, 1537), (3, 6144), (3, 8200), (3, 16400)])
+def test_mean_of_offset_rows(m, T, d):
+    """Rows far from 0 next to their spread, fp32: the mean is off by its own rounding and those of the differences from the
+    pivot, not by those of the sum.  |x - pivot| <= |x - mean| + 80 U |mean|; each of them is rounded once, summed by a chain of
+    80 and divided (4 roundings); pivot + m is rounded once."""
+    g = torch.Generator().manual_seed(d)
+    x = 30000 + torch.randn((T, d), generator=g) * torch.tensor([1.0, 2.0 ** -4, 8.0, 1.0, 1.0])[:T, None]
+    _, stats = run_forward(m, 1, 2, x, None, None)
+    x8 = x.double()
+    mean = x8.mean(1)
+    spread = (x8 - mean[:, None]).abs().mean(1)
+    tol = ops64.U * mean.abs() + 85 * ops64.U * (spread + 80 * ops64.U * mean.abs())
+    ops64.assert_close(stats[:, 0], mean, tol, "mean")
