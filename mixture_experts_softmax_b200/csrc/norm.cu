@@ -838,8 +838,9 @@ RingPlan ring_plan(int T, int nv, int NV, bool warp, int P, int columns, int pla
 inline cudaError_t launch_ring(void (*kernel)(NormArgs, int), const RingPlan &r, const NormArgs &a, int P, cudaStream_t s)
 {
     if (r.smem > 40 * 1024) {   // near the 48 KB that need no leave, static arrays included
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(r.smem));
+        // always the most that any width takes: the limit is the kernel's, shared by all calls, and one that set its own
+        // would take the larger limit of another thread's call away before that call's launch
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return e;

@@ -1,5 +1,7 @@
 """RMSNorm and LayerNorm rows and their gradients (moe_norm_forward, moe_norm_backward) against plain
 64-bit forms: rows held by a warp, by a block and read again, every vector width and type."""
+import threading
+
 import pytest
 import torch
 
@@ -228,3 +230,34 @@ def test_mean_of_offset_rows(m, T, d):
     spread = (x8 - mean[:, None]).abs().mean(1)
     tol = ops64.U * mean.abs() + 85 * ops64.U * (spread + 80 * ops64.U * mean.abs())
     ops64.assert_close(stats[:, 0], mean, tol, "mean")
+
+
+def test_host_threads_at_once(m):
+    """Backward calls from four host threads, each on its own stream, of two widths that take the same kernel with different amounts
+    of shared memory: no call disturbs another's launch, and the results are those of a call alone."""
+    cases = []
+    for d in (4096, 6144) * 2:
+        x, gain, bias, dy = inputs(16, d, 2, True)
+        _, stats = run_forward(m, 1, 2, x, gain, bias)
+        want = run_backward(m, 1, 2, x, gain, stats, dy, True)
+        ins = [t.cuda() for t in (x, gain, stats, dy)]
+        outs = [torch.empty((16, d), device="cuda"), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")]
+        ws = torch.empty(m.moe_norm_workspace(16, d), dtype=torch.uint8, device="cuda")
+        cases.append((d, want, ins, outs, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    status = []
+
+    def work(d, want, ins, outs, ws, stream):
+        # addresses: the calls follow one another as closely as the host allows
+        args = [t.data_ptr() for t in (*ins, *outs, ws)] + [stream.cuda_stream]
+        status.append({m.moe_norm_backward(1, 2, 16, d, *args) for _ in range(20000)})
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{m.MOE_OK}] * 4
+    for d, want, ins, outs, ws, stream in cases:
+        for got, ref in zip(outs, want):
+            assert torch.equal(got.cpu(), ref)
