@@ -973,7 +973,7 @@ extern "C" MOE_API int moe_norm_backward(int kind, int dtype, int T, int d, cons
     if (!op_aligned16(dgain) || !op_aligned16(dbias) || !op_aligned16(gain)) return MOE_EINVAL;
     const size_t row = static_cast<size_t>(d) * dtype_size(dtype), all = T * row, sb = static_cast<size_t>(T) * 8;
     const size_t gb = static_cast<size_t>(d) * 4, wb = static_cast<size_t>(parts_for(T, d)) * 2 * d * 4;
-    if (op_overlap(dgain, gb, dbias, gb)) return MOE_EINVAL;
+    if (op_overlap(dgain, gb, dbias, gb) || op_overlap(dgain, gb, gain, row) || op_overlap(dbias, gb, gain, row)) return MOE_EINVAL;
     if (T > 0) {
         if (!op_ptr(x) || !op_ptr(stats) || !op_ptr(dy) || !op_ptr(dx) || !op_ptr(workspace)) return MOE_EINVAL;
         const struct {

@@ -631,12 +631,19 @@ extern "C" MOE_API int moe_sort_rows(int dtype, int T, int k, int E, int d, cons
     if (T > 0) {
         if (!op_ptr(idx) || !op_ptr(perm) || !op_ptr(slot)) return MOE_EINVAL;
         if (!x != !rows) return MOE_EINVAL;   // both, or the order alone
-        if (x && (!op_ptr(x) || !op_ptr(rows) || op_overlap(x, T * row, rows, n * row))) return MOE_EINVAL;
-        // the order is read from idx by every block while others write it
-        const size_t nb = n * 4, eb = (static_cast<size_t>(E) + 1) * 4;
-        if (op_overlap(idx, nb, perm, nb) || op_overlap(idx, nb, slot, nb) || op_overlap(perm, nb, slot, nb) ||
-            op_overlap(idx, nb, offsets, eb) || op_overlap(perm, nb, offsets, eb) || op_overlap(slot, nb, offsets, eb))
-            return MOE_EINVAL;
+        if (x && (!op_ptr(x) || !op_ptr(rows))) return MOE_EINVAL;
+        // blocks read idx, x and the slots while others write the order and the rows
+        const struct {
+            const void *p;
+            size_t n;
+        } in[] = {{x, T * row}, {idx, n * 4}},
+          out[] = {{offsets, (static_cast<size_t>(E) + 1) * 4}, {perm, n * 4}, {slot, n * 4}, {rows, n * row}};
+        for (int i = 0; i < 4; ++i) {
+            for (const auto &b : in)
+                if (op_overlap(out[i].p, out[i].n, b.p, b.n)) return MOE_EINVAL;
+            for (int j = 0; j < i; ++j)
+                if (op_overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_EINVAL;
+        }
     }
     const int rc = op_device();
     if (rc != MOE_OK) return rc;

@@ -143,3 +143,27 @@ def test_w4_matvec_refusals(m, ran):
         assert m.moe_w4_matvec(**{**good, name: bad}) == m.MOE_EUNSUPPORTED, name
     assert m.moe_w4_matvec(**{**good, "E": 1, "offsets": None, "packed_v": None}) in ran
     assert m.moe_w4_matvec(**{**good, "R": 0, "x": None}) == m.MOE_OK
+
+
+def test_sort_rows_refuses_every_overlap(m, ran):
+    """Each output against each input and each other output, from its first byte, from its end and from its middle."""
+    good = dict(dtype=m.MOE_BF16, T=4, k=2, E=8, d=64, x=addr(0), idx=addr(1), offsets=addr(2), perm=addr(3), slot=addr(4),
+                rows=addr(5), stream=0)
+    size = dict(x=4 * 64 * 2, idx=4 * 2 * 4, offsets=9 * 4, perm=4 * 2 * 4, slot=4 * 2 * 4, rows=8 * 64 * 2)
+    for out in ("offsets", "perm", "slot", "rows"):
+        for other in set(size) - {out}:
+            last = (size[other] - 1) // 16 * 16
+            for at in {0, 16, last}:
+                assert m.moe_sort_rows(**{**good, out: good[other] + at}) == m.MOE_EINVAL, (out, other, at)
+            assert m.moe_sort_rows(**{**good, out: good[other] + (size[other] + 15) // 16 * 16}) in ran, (out, other)
+    # the order alone has no rows to overlap
+    assert m.moe_sort_rows(**{**good, "x": None, "rows": None, "d": 65536}) in ran
+
+
+def test_norm_backward_refuses_overlaps_without_rows(m):
+    """T == 0 still writes the gradients of gain and bias."""
+    good = dict(kind=m.MOE_NORM_LAYER, dtype=m.MOE_BF16, T=0, d=64, x=None, gain=addr(0), stats=None, dy=None, dx=None, dgain=addr(1),
+                dbias=addr(2), workspace=None, stream=0)
+    for name in ("dgain", "dbias"):
+        for at in (addr(0), addr(0) + 112, addr(3 - {"dgain": 1, "dbias": 2}[name]) + 240):
+            assert m.moe_norm_backward(**{**good, name: at}) == m.MOE_EINVAL, (name, at)
