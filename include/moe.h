@@ -552,7 +552,7 @@ MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t *q, const v
  * and with packed_v the gated up-projection, gelu(x W) * (x Wv) with the tanh form of gelu.
  *   x         dtype [R, K]      MOE_BF16 or MOE_F16
  *   offsets   int32 [E+1]       the experts' row ranges, on the device (moe_sort_rows writes them); values
- *                               outside [0, R] are clamped, a row in two ranges gets either product;
+ *                               outside [0, R] are clamped, a row in several ranges gets the first one's product;
  *                               NULL with E == 1: all rows
  *   packed, packed_v            from moe_w4_pack with the same E, K, N, group; packed_v may be NULL
  *   y         out_dtype [R, N]  out: dtype or MOE_F32; rows of no expert are left as they were

@@ -361,9 +361,9 @@ __device__ __forceinline__ float gelu_of(float a)
     return a / (1.f + expf(-2.f * z));
 }
 
-// One pass over the block's share of the weights for up to 8 NB rows.
+// One pass over the block's share of the weights for up to 8 NB rows.  own: a bit for each row that is the expert's to write.
 template <class T, int G, bool GATED, int NB>
-__device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int row0, int rows)
+__device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int row0, int rows, unsigned own)
 {
     constexpr int kGroups = kUnitK / G;                       // of a unit
     constexpr int kStageBytes = kUnitBytes + kGroups * 64;
@@ -457,7 +457,7 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     for (int i = split * (kWarps * 32) + threadIdx.x; i < rows * width; i += a.splits * (kWarps * 32)) {
         const int n = i / width, f = i - n * width;           // width: a power of two times 32
         const int feature = tile * width + f;
-        if (feature >= a.N) continue;
+        if (feature >= a.N || !(own >> n & 1)) continue;
         float v[2] = {0.f, 0.f};
         for (int s = 0; s < a.splits; ++s) {
             const float *src = a.splits > 1 ? cl.map_shared_rank(red, s) : red;
@@ -476,9 +476,11 @@ __device__ __forceinline__ void w4_pass(const W4Args &a, char *smem, int e, int 
     else __syncthreads();
 }
 
-// the n-th expert that has rows, and its rows; the whole warp asks together
-__device__ __forceinline__ bool busy_expert(const W4Args &a, int n, int &e, int &r0, int &r1)
+// the n-th expert that has rows, and its rows; the whole warp asks together.  falls: the offsets go down somewhere so far
+// (or in the same 32), which is the only way for an earlier range to hold one of these rows
+__device__ __forceinline__ bool busy_expert(const W4Args &a, int n, int &e, int &r0, int &r1, bool &falls)
 {
+    falls = false;
     if (!a.offsets) {
         e = 0;
         r0 = 0;
@@ -491,8 +493,10 @@ __device__ __forceinline__ bool busy_expert(const W4Args &a, int n, int &e, int 
         int lo = 0, hi = 0;
         if (mine < a.E) {
             lo = max(__ldg(a.offsets + mine), 0);
-            hi = min(__ldg(a.offsets + mine + 1), a.R);
+            hi = __ldg(a.offsets + mine + 1);
         }
+        falls |= __any_sync(0xffffffffu, hi < lo);
+        hi = min(hi, a.R);
         unsigned m = __ballot_sync(0xffffffffu, lo < hi);
         const int here = __popc(m);
         if (n < here) {
@@ -508,6 +512,16 @@ __device__ __forceinline__ bool busy_expert(const W4Args &a, int n, int &e, int 
     return false;
 }
 
+// the rows r0 .. r0 + 31 that no earlier expert's range holds, a bit each: a row in several ranges is the first one's,
+// whichever block comes first
+__device__ __forceinline__ unsigned rows_owned(const int *offsets, int e, int r0)
+{
+    const int r = r0 + (threadIdx.x & 31);
+    bool mine = true;
+    for (int i = 0; i < e; ++i) mine &= r < __ldg(offsets + i) || r >= __ldg(offsets + i + 1);
+    return __ballot_sync(0xffffffffu, mine);
+}
+
 // MAXNB: the most slabs of 8 rows an expert can have (1, 2, or 4: any number); fewer leave the registers to the others.
 template <class T, int G, bool GATED, int MAXNB>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
@@ -518,20 +532,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(W4Args a)
     // every expert that can have work, not for every expert.
     for (int i = blockIdx.y;; i += gridDim.y) {
         int e, r0, r1;
-        if (!busy_expert(a, i, e, r0, r1)) return;
+        bool falls;
+        if (!busy_expert(a, i, e, r0, r1, falls)) return;
         for (; r0 < r1; r0 += 32) {
             const int rows = min(r1 - r0, 32);
+            const unsigned own = falls ? rows_owned(a.offsets, e, r0) : ~0u;
             if (MAXNB == 1 || rows <= 8) {
-                w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows);
+                w4_pass<T, G, GATED, 1>(a, w4_smem, e, r0, rows, own);
                 continue;
             }
             if constexpr (MAXNB > 1) {
                 if (MAXNB == 2 || rows <= 16) {
-                    w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows);
+                    w4_pass<T, G, GATED, 2>(a, w4_smem, e, r0, rows, own);
                     continue;
                 }
             }
-            if constexpr (MAXNB > 2) w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows);
+            if constexpr (MAXNB > 2) w4_pass<T, G, GATED, 4>(a, w4_smem, e, r0, rows, own);
         }
     }
 }

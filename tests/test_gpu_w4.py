@@ -291,3 +291,24 @@ def test_longest_sides(m, K, N):
     x = torch.randn((2, K), generator=torch.Generator().manual_seed(0)).to(torch.float16)
     ref, tol = ops64.w4(x, [0, 2], [pk], 128, torch.float32)
     check_rows(run(m, 1, 2, x, None, [pk], 128, (1, K, N)), ref, tol)
+
+
+@pytest.mark.parametrize("offsets", [[0, 1, 0, 1, 0, 2], [0, 2, 1, 2, 0, 2], [1, 2, 0, 2, 0, 1], [-5, 1, -2 ** 31, 2 ** 31 - 1, 0, 2],
+                                     [2, 0, 1, 0, 2, 2], [30, 38, 0, 40, 20, 40], [40, 3, 5, 0, 33, 1]])
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_row_in_several_ranges_is_the_first_one_s(m, offsets, gated):
+    """Offsets that go down and up again: a row that several ranges hold gets the first one's product, over all tiles of a wide
+    product, and the same bits every time; a row that one range holds gets that one's."""
+    E, R, K, N = 5, max(2, min(max(offsets), 40)), 500, 4100
+    packs = [weights(E, K, N, 64, s) for s in (4, 5)[:1 + gated]]
+    x = torch.randn((R, K), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    ref, tol = (torch.full((R, N), float("nan"), dtype=ops64.F8) for _ in range(2))
+    for e in reversed(range(E)):   # the first range last
+        lo, hi = max(offsets[e], 0), min(offsets[e + 1], R)
+        if lo < hi:
+            y, t = ops64.w4(x, [0] * e + [lo] + [hi] * (E - e), packs, 64, torch.float32)
+            ref[lo:hi], tol[lo:hi] = y[lo:hi], t[lo:hi]
+    got = [run(m, 0, 2, x, offsets, packs, 64, (E, K, N)) for _ in range(10)]
+    check_rows(got[0], ref, tol)
+    for again in got[1:]:
+        assert torch.equal(again, got[0])
