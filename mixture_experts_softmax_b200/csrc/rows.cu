@@ -232,7 +232,7 @@ struct CopyArgs {
 
 // perm: nullptr, or where the first unit of a token notes its routes
 template <class V, class S>
-__device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long unit, S &&slot_of, bool wait, int *perm)
+__device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long unit, S &&slot_of, int *perm)
 {
     const int lanes = 1 << c.lg, lane = threadIdx.x & (lanes - 1);
     const bool on = unit < c.units;
@@ -243,7 +243,6 @@ __device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long 
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
         if (v0 + u * lanes < c.vpr) v[u] = __ldg(src + v0 + u * lanes);
-    if (wait) op_begin();   // x is older than the order's launch, which had waited before this one could begin
     if (!on) return;
     for (int j0 = 0; j0 < k; j0 += kUnroll) {
         int row[kUnroll];
@@ -264,9 +263,9 @@ __device__ __forceinline__ void copy_unit(const CopyArgs &c, int k, int n, long 
 template <class V>
 __global__ void __launch_bounds__(256) sort_copy_kernel(CopyArgs c, const int *slot, int k, int n, int *perm)
 {
+    op_begin();   // before x too: its writer ended before the order's launch began, but only a thread's own wait shows it x
     const long unit = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) >> c.lg;
-    // plain loads: the slots are written while this kernel may already run
-    copy_unit<V>(c, k, n, unit, [&](int r) { return *reinterpret_cast<const volatile int *>(slot + r); }, true, perm);
+    copy_unit<V>(c, k, n, unit, [&](int r) { return __ldg(slot + r); }, perm);
 }
 
 // A small batch in one launch: every block finds the whole order by itself (it is a few steps of
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) sort_small_kernel(SortArgs a
     __syncthreads();
     if (!c.x) return;
     const long unit = (static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x) >> c.lg;
-    copy_unit<V>(c, a.k, a.n, unit, [&](int r) { return slots[r]; }, false, nullptr);
+    copy_unit<V>(c, a.k, a.n, unit, [&](int r) { return slots[r]; }, nullptr);
 }
 
 // lanes of a unit and units of a row for rows of vpr vectors: short rows share a warp

@@ -297,3 +297,25 @@ def test_sort_four_million_routes(m):
     want[order[:n]] = torch.arange(n, device="cuda")
     assert torch.equal(slot.flatten().long(), want)
     assert torch.equal(rows[:n, 0].long(), order[:n] // k) and (rows[n:] == -1).all()
+
+
+@pytest.mark.parametrize("T,d", [(3000, 1024), (700, 6144), (400, 256)])
+def test_sort_right_behind_the_writer_of_x(m, T, d):
+    """One buffer of tokens, written anew on the device right before every sort of it, with no wait between: the rows are always
+    the last tokens'."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    hs = [torch.randn((T, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(5)]
+    want = [torch.empty_like(h) for h in hs]
+    for h, u in zip(hs, want):
+        m.check(m.moe_norm_forward(m.MOE_NORM_RMS, 0, T, d, h, None, None, 1e-5, u))
+    idx = torch.rand((T, 8), generator=g, device="cuda").argsort(1)[:, :2].to(torch.int32).contiguous()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offsets, perm, slot = torch.empty(9, **i32), torch.empty(2 * T, **i32), torch.empty((T, 2), **i32)
+    x, rows = torch.empty_like(hs[0]), [torch.empty((2 * T, d), dtype=torch.bfloat16, device="cuda") for _ in range(40)]
+    torch.cuda.synchronize()
+    for turn, out in enumerate(rows):
+        m.check(m.moe_norm_forward(m.MOE_NORM_RMS, 0, T, d, hs[turn % 5], None, None, 1e-5, x))
+        m.check(m.moe_sort_rows(0, T, 2, 8, d, x, idx, offsets, perm, slot, out))
+    at = perm.long() // 2
+    for turn, out in enumerate(rows):
+        assert torch.equal(out, want[turn % 5][at]), turn
