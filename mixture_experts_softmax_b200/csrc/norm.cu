@@ -991,9 +991,8 @@ extern "C" MOE_API int moe_norm_backward(int kind, int dtype, int T, int d, cons
     if (rc != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {   // no rows: the sums are 0
-        if (dgain && cudaMemsetAsync(dgain, 0, gb, s) != cudaSuccess) return MOE_ECUDA;
-        if (dbias && cudaMemsetAsync(dbias, 0, gb, s) != cudaSuccess) return MOE_ECUDA;
-        return MOE_OK;
+        const int done = dgain ? op_status(cudaMemsetAsync(dgain, 0, gb, s)) : MOE_OK;
+        return done == MOE_OK && dbias ? op_status(cudaMemsetAsync(dbias, 0, gb, s)) : done;
     }
     NormArgs a{T, d, x, gain, nullptr, 0.f, nullptr, const_cast<float *>(stats), dy, dx, static_cast<float *>(workspace),
                dgain, dbias};

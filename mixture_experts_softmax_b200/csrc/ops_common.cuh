@@ -33,6 +33,14 @@ inline bool op_overlap(const void *a, size_t na, const void *b, size_t nb)
 inline size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F16 || dtype == MOE_F32; }
 
+// the status of a runtime call; a failure is reported through it and not left behind for the next call to report again
+inline int op_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return MOE_OK;
+    cudaGetLastError();
+    return MOE_ECUDA;
+}
+
 // MOE_OK if the current device can run the library's sm_100a code
 int op_device();
 

@@ -591,8 +591,6 @@ int by_types(int rows_dtype, int dtype, F &&f)
 
 bool sizes_ok(int T, int k, int d) { return T >= 0 && T <= MOE_MAX_TOKENS && k >= 1 && k <= kMaxPicks && d >= 1 && d <= 65536; }
 
-int status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ECUDA; }
-
 }  // namespace
 
 int op_device()
@@ -646,12 +644,12 @@ extern "C" MOE_API int moe_sort_rows(int dtype, int T, int k, int E, int d, cons
     }
     const int rc = op_device();
     if (rc != MOE_OK) return rc;
-    if (T == 0) return status(cudaMemsetAsync(offsets, 0, (static_cast<size_t>(E) + 1) * 4, s));
+    if (T == 0) return op_status(cudaMemsetAsync(offsets, 0, (static_cast<size_t>(E) + 1) * 4, s));
     const SortArgs a{T, k, E, static_cast<int>(n), idx, offsets, perm, slot};
-    if (row % 16 == 0) return status(launch_sort<uint4>(a, x, rows, row, s));
-    if (row % 8 == 0) return status(launch_sort<uint2>(a, x, rows, row, s));
-    if (row % 4 == 0) return status(launch_sort<uint32_t>(a, x, rows, row, s));
-    return status(launch_sort<uint16_t>(a, x, rows, row, s));
+    if (row % 16 == 0) return op_status(launch_sort<uint4>(a, x, rows, row, s));
+    if (row % 8 == 0) return op_status(launch_sort<uint2>(a, x, rows, row, s));
+    if (row % 4 == 0) return op_status(launch_sort<uint32_t>(a, x, rows, row, s));
+    return op_status(launch_sort<uint16_t>(a, x, rows, row, s));
 }
 
 extern "C" MOE_API int moe_unsort_rows(int rows_dtype, int dtype, int T, int k, int d, const void *rows,
@@ -669,7 +667,7 @@ extern "C" MOE_API int moe_unsort_rows(int rows_dtype, int dtype, int T, int k, 
     if (rc != MOE_OK) return rc;
     const UnsortArgs a{T, k, d, rows, slot, gate, out};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return by_types(rows_dtype, dtype, [&](auto r, auto o) { return status(unsort_by_width<decltype(r), decltype(o)>(a, s)); });
+    return by_types(rows_dtype, dtype, [&](auto r, auto o) { return op_status(unsort_by_width<decltype(r), decltype(o)>(a, s)); });
 }
 
 extern "C" MOE_API int moe_unsort_rows_backward(int rows_dtype, int dtype, int T, int k, int d, const void *dout,
@@ -694,5 +692,5 @@ extern "C" MOE_API int moe_unsort_rows_backward(int rows_dtype, int dtype, int T
     const UnsortGradArgs a{T, k, d, dout, rows, slot, gate, drows, dgate};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_types(rows_dtype, dtype,
-                    [&](auto r, auto o) { return status(unsort_grad_by_width<decltype(r), decltype(o)>(a, s)); });
+                    [&](auto r, auto o) { return op_status(unsort_grad_by_width<decltype(r), decltype(o)>(a, s)); });
 }

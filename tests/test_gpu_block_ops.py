@@ -1,6 +1,7 @@
 """The stand-alone operators together, as a program uses them: the residual MoE block with 4-bit experts for a few
 tokens (norm, routing, sort, gated product, product, back with gates), eagerly and as a replayed CUDA graph,
 and a training step of a block with a program's own experts."""
+import ctypes
 import math
 
 import pytest
@@ -301,3 +302,31 @@ def test_calls_right_behind_one_another(m):
     for _ in range(3):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
+
+
+def test_a_refused_call_leaves_no_error_behind(m):
+    """A call that the runtime refuses (on the legacy stream while another stream is being captured) returns MOE_ECUDA and is
+    over with it: the next call of any entry point does not report it again."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    s, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert cu.cuStreamCreate(ctypes.byref(s), 0) == 0   # a stream that the legacy stream waits for
+    T, d = 64, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x, w = torch.ones((T, d), dtype=torch.bfloat16, device="cuda"), torch.ones((d, 8), device="cuda")
+    idx, offsets, perm, gate = (torch.empty((T, 2), **i32), torch.empty(9, **i32), torch.empty(2 * T, **i32),
+                                torch.empty((T, 2), device="cuda"))
+    g = torch.ones(d, device="cuda")
+    calls = {"sort": lambda: m.moe_sort_rows(0, 0, 2, 8, d, None, None, offsets, None, None, None, 0),
+             "norm": lambda: m.moe_norm_backward(0, 0, 0, d, None, None, None, None, None, g, None, None, 0)}
+    m.check(m.moe_route_noalloc(T, d, x, w, None, idx, gate, offsets, perm))
+    for name, call in calls.items():
+        torch.cuda.synchronize()
+        assert cu.cuStreamBeginCapture_v2(s, 0) == 0   # 0: the mode that forbids this everywhere
+        try:
+            assert call() == m.MOE_ECUDA, name
+        finally:
+            assert cu.cuStreamEndCapture(s, ctypes.byref(graph)) != 0   # the call ended the capture
+        assert m.moe_route_noalloc(T, d, x, w, None, idx, gate, offsets, perm) == m.MOE_OK, name
+        torch.cuda.synchronize()
+    assert cu.cuStreamDestroy_v2(s) == 0
