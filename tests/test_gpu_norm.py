@@ -261,3 +261,27 @@ def test_host_threads_at_once(m):
     for d, want, ins, outs, ws, stream in cases:
         for got, ref in zip(outs, want):
             assert torch.equal(got.cpu(), ref)
+
+
+@pytest.mark.parametrize("T,d", [(12, 37), (12, 300), (12, 301), (40, 1537), (12, 8200), (12, 16401)])
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dt", [0, 2])
+def test_nonfinite_gradient_rows_stay_in_their_row(m, T, d, kind, dt):
+    """nan and inf at both ends and inside of some rows of x and dy, next to rows that share their 16-byte vectors: the other rows'
+    dx does not change by a bit, and a column's sums are nan only where a bad row is in it."""
+    x, gain, bias, dy = inputs(T, d, dt, kind == 1)
+    _, stats = run_forward(m, kind, dt, x, gain, bias)
+    want = run_backward(m, kind, dt, x, gain, stats, dy, kind == 1)
+    bad = {2: (x, float("nan")), 5: (dy, float("inf")), 8: (dy, float("nan"))}
+    for row, (t, v) in bad.items():
+        t[row, [0, d // 2, d - 1]] = v
+    got = run_backward(m, kind, dt, x, gain, stats, dy, kind == 1)
+    ok = [t for t in range(T) if t not in bad]
+    assert torch.equal(got[0][ok], want[0][ok])
+    for row in bad:
+        assert not got[0][row].isfinite().any()
+    cols = torch.ones(d, dtype=torch.bool)
+    cols[[0, d // 2, d - 1]] = False
+    for a, b in list(zip(got, want))[1:2 + kind]:
+        assert torch.equal(a[cols], b[cols])
+        assert not a[~cols].isfinite().any()

@@ -312,3 +312,17 @@ def test_a_row_in_several_ranges_is_the_first_one_s(m, offsets, gated):
     check_rows(got[0], ref, tol)
     for again in got[1:]:
         assert torch.equal(again, got[0])
+
+
+@pytest.mark.parametrize("power", [-90, -93, -96])
+@pytest.mark.parametrize("rows,group", [(3, 32), (5, 128), (20, 64)])
+def test_small_bf16_inputs_lose_nothing(m, power, rows, group):
+    """Inputs between 2^-100 and some 2^power, whose products are subnormal sums in multiples of 2^-149: only the usual
+    roundings.  A result of 0 would fail."""
+    K = 1000
+    q, s = weights(1, K, 96, group, 24)
+    x = (torch.randn((rows, K), generator=torch.Generator().manual_seed(7)) * 2.0 ** power).to(torch.bfloat16)
+    x = torch.where(x.abs() < 2.0 ** -100, 0, x)
+    ref, tol = ops64.w4(x, [0, rows], [(q, s)], group, torch.float32)
+    assert (tol < ref.abs() / 8).double().mean() > 0.9
+    check_rows(run(m, 0, 2, x, None, [(q, s)], group, (1, K, 96)), ref, tol)
