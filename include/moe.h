@@ -447,6 +447,7 @@ MOE_API int moe_route_noalloc(int T, int d, const void *x, const float *router_w
  *     calls, and must not be shared by calls that may run at the same time;
  *   - the device that holds the tensors must be the current one, and the stream one of its streams;
  *   - results do not depend on scheduling: the same inputs give the same bits;
+ *   - several host threads may call them at the same time;
  *   - an output must not overlap an input or another output (MOE_EINVAL).
  * Common errors: MOE_EINVAL for a bad size or type, a missing or misaligned (16 bytes) pointer;
  * MOE_ENODEV without an sm_100 device; MOE_ECUDA if a launch failed.
@@ -489,7 +490,7 @@ MOE_API int moe_unsort_rows(int rows_dtype, int dtype, int T, int k, int d, cons
  * The gradient of moe_unsort_rows:
  *   drows[slot[t,j]] = gate[t,j] * dout[t],   dgate[t,j] = sum_c dout[t,c] * rows[slot[t,j],c]
  *   dout   dtype [T, d]
- *   rows   rows_dtype [T*k, d]  the forward call's rows; may be NULL when dgate is
+ *   rows   rows_dtype [T*k, d]  the forward call's rows; may be NULL when dgate is, and is not looked at then
  *   drows  rows_dtype [T*k, d]  out; rows that no route points to are left as they were
  *   dgate  fp32 [T, k]          out, 0 for a dropped route; NULL: not wanted
  * No two routes may have the same slot.
@@ -560,7 +561,8 @@ MOE_API int moe_w4_pack(int E, int K, int N, int group, const int8_t *q, const v
  * MOE_EUNSUPPORTED).  R == 0 is a no-op.  Sums are fp32.  A group's products are summed with the weights offset by 8 and
  * the offset taken off again, so where all weights are 0 the result is a rounding of the inputs' sum (about 2^-24
  * of it), not an exact 0.  Infinite and nan inputs follow the formula.  A bf16 input below 2^-100 counts with an
- * absolute error of up to 2^-112, and the scales are below 2^94.
+ * absolute error of up to 2^-112, and the scales are below 2^94.  A row's last bits can depend on the other rows of
+ * its call: on their number, and on whether one holds a value that the offset form cannot (bf16 from 2^27 up, inf, nan).
  */
 MOE_API int moe_w4_matvec(int dtype, int out_dtype, int E, int K, int N, int group, int R, const void *x,
                           const int32_t *offsets, const void *packed, const void *packed_v, void *y, void *stream);

@@ -18,9 +18,10 @@
 // Rows too wide for a block's registers are read again from the caches instead, with the columns' sums in shared memory
 // or, wider still, taken by a kernel of their own.
 //
-// Measured on a B200: LayerNorm of 16,383 x 2560 fp32 53 us (98% of the copy bandwidth), RMSNorm gradient of 8192 x
-// 6144 bf16 66 us (71%: about 60 us for the rows, at half of all issue slots, and the reduction), LayerNorm
-// gradient of 5003 x 1537 fp16 31 us (23%: each block waits for one row's sums after the other, some 2700 cycles a row).
+// Measured on a B200: LayerNorm of 16,383 x 2560 fp32 53 to 57 us (91 to 98% of the copy bandwidth), of 8192 x 1537 fp16 22.5 us
+// (34%), RMSNorm of the same 18.4; RMSNorm gradient of 8192 x 6144 bf16 66 us (71%: about 60 us for the rows, at 48% of all issue
+// slots, and the reduction), LayerNorm gradient of 5003 x 1537 fp16 30 us (24%: each block waits for one row's sums after
+// the other, some 2700 cycles a row).
 #include "ops_common.cuh"
 
 namespace moe {
@@ -829,8 +830,10 @@ RingPlan ring_plan(int T, int nv, int NV, bool warp, int P, int columns, int pla
     grid = grid < work ? grid : work;
     grid = grid < most ? grid : most;
     r.grid = (grid + P - 1) / P * P;
-    // several blocks an SM, but fewer than fit, would spread unevenly beside a predecessor's last blocks
-    // (gradient of 5003 x 1537 fp16: 36.5 us against 31.3)
+    // Several blocks an SM, but fewer than fit, would spread unevenly beside a predecessor's last blocks.  Gradients, us, with
+    // the early start against without: 5003 x 1537 fp16 35.8 and 30.8, 1500 x 2560 bf16 29.2 and 24.3, 2000 x 1537 fp16 23.2 and
+    // 21.0 (but 4000 x 1024 bf16 18.7 and 19.7); where the rule starts early: 8192 x 6144 bf16 66.3 and 68.2, 500 x 6144 19.7 and
+    // 20.9, forward of 8192 x 1537 fp16 22.5 and 25.0.
     r.early = r.grid <= kSms || grid >= kSms * occ;
     return r;
 }

@@ -166,10 +166,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) sort_plan_kernel(SortArgs a, 
     op_begin();
 
     const int per = ((a.n + C * kPlanWarps - 1) / (C * kPlanWarps) + 31) / 32 * 32;
-    // long: the last warps' segments may begin behind the end of the range of an int
-    const long b0 = static_cast<long>(rank * kPlanWarps + warp) * per;
-    const int begin = static_cast<int>(b0 < a.n ? b0 : a.n);
-    const int end = static_cast<int>(b0 + per < a.n ? b0 + per : a.n);
+    // n is 2^22 at most, and the last segment begins less than 8500 behind its end
+    const int begin = min((rank * kPlanWarps + warp) * per, a.n), end = min(begin + per, a.n);
     for (int i = threadIdx.x; i < kPlanStride * a.E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
     count_segment(a, begin, end, cnt + warp, kPlanStride, a.slot);   // ranks where the rows will stand

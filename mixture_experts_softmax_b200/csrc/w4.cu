@@ -10,11 +10,11 @@
 // multiplied by the group's scale and added up in fp32.  (The tcgen05 path wants both operands
 // staged as 16-bit tiles; for 8 columns that staging alone moves four times the weights' bytes through shared memory.)
 //
-// Measured on a B200: gated up-projection of 16 rows over 8 experts of 6144 x 32768 (1.66 GB) 268 us at full clock, 94 to 96%
-// of the copy bandwidth, and 314 to 328 us once the power limit holds the clock near 1.57 GHz (then the integer pipe
-// is what bounds it); down-projection of one row each over 2 experts of 32768 x 6144 49 us, 67%: its 48 tiles,
-// cut 5 times, fill the SMs' places once, unevenly.  More rows cost more multiplies and x traffic: one expert of 6144 x
-// 32768, gated, takes 41, 46, 80 and 134 us for 1, 8, 16 and 32 rows.
+// Measured on a B200: gated up-projection of 16 rows over 8 experts of 6144 x 32768 (1.66 GB) 267 us at full clock, 96% of the
+// copy bandwidth, and 306 to 331 us once the power limit holds the clock near 1.57 GHz (the integer pipe is the busiest then);
+// down-projection of one row each over 2 experts of 32768 x 6144 48 us, 69%: its 48 tiles, cut 5 times, fill the
+// SMs' places once, unevenly.  More rows cost more multiplies and x traffic: one expert of 6144 x 32768, gated, takes 40, 45, 69
+// and 123 us for 1, 8, 16 and 32 rows, up to 7 and 10 us more for the last two where the power limit holds the clock.
 //
 // Packed layout (moe_w4_pack).  Features in blocks of 32, inputs in units of 128 (padded: value 0,
 // scale 0).  A unit of a block is 2 KB, in the order of the lanes' multiply operands: input chunk of
@@ -165,7 +165,10 @@ __device__ __forceinline__ T2 as16(uint32_t w)
 // those of u - 8; the scale's factor takes the powers of two back.  bf16 inputs are staged at 2^100 times their
 // value, which keeps the products in the normal range.  A phase whose inputs do not allow that (bf16 from 2^27 up,
 // inf, nan) takes the exact form: an FMA per pair makes u - 8 of it, as an ordinary number.
-// At 16 rows over 8 experts of 6144 x 32768, gated: 307 us with the FMAs everywhere.
+// What the fast form costs: sums at the size of 8 times the inputs' sum, about twice the rounding of the plain products (fp32 results of
+// one token down: 7.0e-7 of the largest, plain fp32 products 4.8e-7), and all columns of a pass share one phase's choice.
+// What the exact form everywhere costs, us: 16 rows over 8 experts of 6144 x 32768, gated, 298 against 270; one token over 2
+// experts of 32768 x 6144, fp16, 65 against 48; the decode step's 16 rows there 182 against 161.
 template <class T> struct Deq;
 template <> struct Deq<__nv_bfloat16> {
     static constexpr float kFast[2] = {0x1p33f, 0x1p29f};      // 2^133 / 2^100, and / 16
@@ -560,12 +563,13 @@ constexpr int smem_bytes(int G)
 }
 
 // How a call is cut: kparts warps share a feature block's inputs, `splits` blocks of a cluster the input range.
-// The estimate counts microseconds as measured here: a warp's step (one unit, eight warps a block) takes 0.53 in a block
-// that has an SM to itself and 0.9 where two share one; a block's start and end 3, plus 0.17 for every row of
-// every phase of staged x, plus 2 for a cluster.  slots: blocks that run together, fewer where clusters do not
-// fill the groups of SMs.  Examples (us, chosen and next best of the other kind): 2 experts of 32768 x 6144, one
-// row each, 5 splits 54 against 60 with two warps an input range and 4 splits, 138 with neither;
-// 64 experts of 2048 x 1408, 2 kparts 29.5, 1 kpart 31.6, 2 splits 35.
+// The estimate counts microseconds as measured here with a ring of four stages (three now; it only ranks the cuts): a
+// warp's step (one unit, eight warps a block) takes 0.53 in a block that has an SM to itself and 0.9 where two share one; a
+// block's start and end 3, plus 0.17 for every row of every phase of staged x, plus 2 for a cluster.  slots: blocks that run
+// together, fewer where clusters do not fill the groups of SMs, as measured on one B200.  It takes the rows to be spread over as
+// many experts as can have some; where a batch goes to few of many, more splits would serve it better.  Examples (us): 2
+// experts of 32768 x 6144, one row each, 5 splits (chosen) 48, 4 splits of two warps an input range 54, 2 of two 60, neither
+// 123; 64 experts of 2048 x 1408, 2 kparts (chosen) 28.0, neither 30.1, 2 splits 34.0.
 struct W4Cut {
     int splits, kparts;
 };

@@ -3,6 +3,7 @@ tokens (norm, routing, sort, gated product, product, back with gates), eagerly a
 and a training step of a block with a program's own experts."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -330,3 +331,32 @@ def test_a_refused_call_leaves_no_error_behind(m):
         assert m.moe_route_noalloc(T, d, x, w, None, idx, gate, offsets, perm) == m.MOE_OK, name
         torch.cuda.synchronize()
     assert cu.cuStreamDestroy_v2(s) == 0
+
+
+def test_blocks_of_several_host_threads(m):
+    """Blocks of different sizes run by a host thread each, on streams of their own, give the bits of a block run alone."""
+    blks = [Block4(m, T, d, ffn, group, seed=T) for T, d, ffn, group in ((1, 256, 512, 128), (8, 512, 1024, 64), (33, 264, 328, 32))]
+    streams, want, failed = [torch.cuda.Stream() for _ in blks], [], []
+    for blk in blks:
+        blk.h.copy_(tokens(blk.T, blk.d, blk.T))
+        blk.run()
+        torch.cuda.synchronize()
+        want.append([getattr(blk, k).clone() for k in ("rows", "mid", "y", "out")])
+    torch.cuda.synchronize()
+
+    def work(blk, stream):
+        try:
+            for _ in range(300):
+                blk.experts(stream.cuda_stream)   # the routing stays outside: it shares a scratch array
+        except Exception as e:   # noqa: BLE001 -- the test's own thread reports it
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(blks, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for blk, ref in zip(blks, want):
+        for got, r in zip((blk.rows, blk.mid, blk.y, blk.out), ref):
+            assert torch.equal(got, r)
