@@ -74,9 +74,10 @@ __device__ __forceinline__ float2 row_sums(float s0, float s1, float2 *buf)
 // 39.4 us at 8192 x 6144 bf16, 22.6 to 24.5 at 4097 x 2051 fp32, 52.7 to 52.8 at 16,383 x 2560 fp32.
 __device__ __forceinline__ float corrected(float2 tq, float inv, float &mean)
 {
-    const float m = tq.x * inv, var = fmaf(tq.y, inv, -m * m);
+    const float m = tq.x * inv, v = tq.y * inv, var = fmaf(-m, m, v);
     mean += m;
-    return var < 0.f ? 0.f : var;   // nan stays
+    if (v == __int_as_float(0x7f800000)) return v;   // squares beyond fp32, of m too perhaps; below that m^2 <= v
+    return var < 0.f ? 0.f : var;                    // nan stays
 }
 
 template <class T>

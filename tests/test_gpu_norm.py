@@ -285,3 +285,13 @@ def test_nonfinite_gradient_rows_stay_in_their_row(m, T, d, kind, dt):
     for a, b in list(zip(got, want))[1:2 + kind]:
         assert torch.equal(a[cols], b[cols])
         assert not a[~cols].isfinite().any()
+
+
+@pytest.mark.parametrize("d", [96, 1537, 6144, 8200, 16400, 40001])
+def test_constant_rows_of_huge_values(m, d):
+    """Values whose pivot is off by more than fp32 squares hold: the mean is still the value and y the bias."""
+    x = torch.tensor([3.3e26, -1.7e30, 7.7e18])[:, None].expand(3, d).contiguous()
+    gain, bias = torch.full((d,), 2.0), torch.full((d,), 0.5)
+    y, stats = run_forward(m, 1, 2, x, gain, bias)
+    assert torch.equal(stats[:, 0], x[:, 0])
+    assert (y == 0.5).all()
